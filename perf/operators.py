@@ -200,8 +200,8 @@ def _pack(y, e, fmt, kind):
         z = z[..., 0::2] | (z[..., 1::2] << 4)                     # low nibble first: 8 bytes
         z = z.unflatten(-3, (nb // 2, 2)).transpose(-3, -2)        # [sub][b/2][lane][b%2][8]
     z = z.reshape(*lead, t, -1)
-    s = (e + 127).to(torch.uint8).reshape(*lead, t, TILE * nb)
-    return torch.cat([z, s], -1).contiguous()
+    s = (e + 127).to(torch.uint8).reshape(*lead, t, 8, 4, nb).transpose(-2, -1)    # [quad of tokens][b][token]
+    return torch.cat([z, s.reshape(*lead, t, TILE * nb)], -1).contiguous()
 
 
 def _unpack(tiles, D, fmt, kind):
@@ -221,7 +221,8 @@ def _unpack(tiles, D, fmt, kind):
         z = z.reshape(*lead, t, 2, nb, 8, 4, 4, 4)                 # sub b g c j t
         p = [n, n + 3, n + 5, n + 1, n + 2, n + 4]
     code = z.permute(*range(n), *p).reshape(*lead, t * TILE, D)
-    e = s.reshape(*lead, t * TILE, nb).float() - 127
+    e = s.reshape(*lead, t, 8, nb, 4).transpose(-2, -1)
+    e = e.reshape(*lead, t * TILE, nb).float() - 127
     return _values(_from_codes(code, fmt), e)
 
 
