@@ -551,6 +551,156 @@ LOOPVQ_API loopvq_status loopvq_residual_decode_attn(const loopvq_residual_desc*
                                                      float* out, float* lse_out, void* workspace,
                                                      size_t workspace_bytes, loopvq_stream_t stream);
 
+/* ------------------------------------------- microscaled KV cache (MX) */
+
+/*
+ * A cache that codes every token the moment it is written, with no codebook
+ * and no token group to wait for: the 8- and 4-bit companion of the coded
+ * caches above for steps or layers that a codebook does not serve, with one
+ * cache per loop step.  32 channels of one token's key or value share one
+ * power-of-two scale (the microscaling formats of the OCP MX specification):
+ *   e   = the least integer in [-64, 56] with max|x| <= top * 2^e
+ *         (-64 for a block of zeros),
+ *   code = the element value nearest to x * 2^-e, ties to the even code,
+ *          larger magnitudes (possible at e = 56 only) to +-top,
+ *   read back: code * 2^e,
+ * with elements e4m3 (top 448, 8.25 bits per element with the scales) or
+ * e2m1 (top 6, 4.25 bits).  All steps are exact but the one rounding.  A
+ * block that holds an infinity or a NaN reads back as 32 NaN.
+ *
+ * Pools (one for K, one for V): [T][H][pool_tokens/32][tile]; a tile is 32
+ * tokens of one head, a multiple of 16 bytes:
+ *   codes:  two halves (sub) of 16 tokens; a half is D/32 blocks (b) of 32
+ *           lanes (g = lane/4, c = lane%4) of 16 codes:
+ *             K  lane (g, c): token 4*(g/2) + g%2 + 2*ab, channel
+ *                32*b + 8*c + i, in the order [ab 0..1][i 0..7];
+ *             V  lane (g, c): token 4*c + t, channel 32*b + 4*g + j, in the
+ *                order [j 0..3][t 0..3];
+ *           e4m3: [sub][b][lane][16 bytes]; e2m1 (two codes a byte, the first
+ *           in the low nibble): [sub][b/2][lane][b%2][8 bytes];
+ *   scales: one byte e + 127 per token and block (255, with codes 0: NaN),
+ *           of token 4*i + t of the tile at [i 0..7][b][t 0..3].
+ * This is the order in which the matrix instructions of loopvq_mx_attn take
+ * their operands.
+ */
+typedef enum { LOOPVQ_MX_E4M3 = 0, LOOPVQ_MX_E2M1 = 1 } loopvq_mx_format;
+
+typedef struct {
+  int32_t n_loop;      /* T */
+  int32_t n_heads_kv;  /* H */
+  int32_t n_heads_q;   /* Hq, a multiple of H */
+  int32_t head_dim;    /* D: 64 or 128 */
+  loopvq_mx_format format;
+} loopvq_mx_desc;
+
+/*
+ * Paged layout of a batch.  Token p of request r sits at pool position
+ *   pages[r * max_pages + p / page_tokens] * page_tokens + p % page_tokens.
+ * Request r's context has ctx_len[r] tokens; its NEW tokens are the last
+ * n_r = new_off[r+1] - new_off[r] of them, and rows new_off[r] ..
+ * new_off[r+1]-1 of every packed argument (x, q, out, tree_mask) are theirs,
+ * in order.  A decode step has n_r = 1, a prompt its whole length, a tree of
+ * drafted tokens its nodes, an idle request 0.
+ * Faults (LOOPVQ_FAULT_* bits ORed into fault_bits, a device uint32 that the
+ * caller zeroes, or NULL): a ctx_len or new_off out of its bounds
+ * (CTX_RANGE) leaves that request out, its rows and tokens as they were; a
+ * page id outside the pool (POOL_RANGE) leaves out that page's tokens.
+ * Pages written in one call must not be shared between its requests.
+ */
+typedef struct {
+  int32_t batch;             /* 1 .. 65535 */
+  int32_t page_tokens;       /* a positive multiple of 32 */
+  int32_t max_pages;         /* row length of pages */
+  int32_t max_ctx_len;       /* host bound on ctx_len[r]; <= max_pages * page_tokens */
+  int32_t max_new;           /* host bound on n_r */
+  int32_t total_new;         /* rows of the packed arguments; new_off[batch] <= total_new */
+  int64_t pool_tokens;       /* a positive multiple of 32 */
+  const int32_t* pages;      /* device [batch][max_pages] */
+  const int32_t* ctx_len;    /* device [batch] */
+  const int32_t* new_off;    /* device [batch + 1] */
+} loopvq_mx_layout;
+
+/* Bytes of one pool (K or V, all loop steps); 0 if desc or pool_tokens is invalid. */
+LOOPVQ_API size_t loopvq_mx_pool_bytes(const loopvq_mx_desc* desc, int64_t pool_tokens);
+
+/*
+ * Quantises the new tokens' keys and values of loop steps first_step ..
+ * first_step + n_steps - 1 into both pools, in one launch.
+ *   k, v    : device, element (s, row, h, d) at s*stride_t + row*stride_n +
+ *             h*stride_h + d (s = step - first_step; strides in elements,
+ *             >= 0, the same for both) in x_dtype; not the pools' memory.
+ *   poolK/V : device, 16-byte aligned.
+ * Tokens that are not new keep their bytes.
+ */
+LOOPVQ_API loopvq_status loopvq_mx_write(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
+                                         int32_t first_step, int32_t n_steps, const void* k, const void* v,
+                                         loopvq_dtype x_dtype, int64_t stride_t, int64_t stride_n,
+                                         int64_t stride_h, void* poolK, void* poolV, uint32_t* fault_bits,
+                                         loopvq_stream_t stream);
+
+/*
+ * Reads the new tokens back: the inverse of loopvq_mx_write with the same
+ * layout (any range of a context is "new" to a layout whose ctx_len is the
+ * range's end).  k_out, v_out: device, in out_dtype, strides as above and > 0
+ * wherever two elements would meet otherwise.
+ */
+LOOPVQ_API loopvq_status loopvq_mx_read(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
+                                        int32_t first_step, int32_t n_steps, const void* poolK, const void* poolV,
+                                        void* k_out, void* v_out, loopvq_dtype out_dtype, int64_t stride_t,
+                                        int64_t stride_n, int64_t stride_h, uint32_t* fault_bits,
+                                        loopvq_stream_t stream);
+
+/* Workspace bytes of loopvq_mx_attn (0 if invalid, at least 256 otherwise). */
+LOOPVQ_API size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout);
+
+/*
+ * Attention of each request's new tokens (at most 64: one token, or a tree or
+ * chain of drafted ones, whose keys and values are in the cache already) over
+ * its context at one loop step.  With P = ctx_len - n_r, new token i sees the
+ * prefix p < P and the new tokens j with bit j of its mask set:
+ *   s = softmax_scale * q . k;  s = softcap * tanh(s / softcap) if softcap > 0;
+ *   s = s - slopes[hq] * (pos_i - pos_n) if slopes is given;
+ *   o = sum_n softmax(s)_n v_n
+ * where a prefix token's position is its index and new token j's is P + the
+ * number of OTHER new tokens that its mask shows (its depth in the tree).
+ *   tree_mask : device uint64 [total_new], or NULL: token i sees 0 .. i.
+ *               A token's own bit is honoured like any other; bits from n_r
+ *               on are ignored.
+ *   q         : device, (row, hq, d) at row*q_stride_n + hq*q_stride_h + d in
+ *               q_dtype.  Query head hq reads KV head hq / (Hq / H).
+ *   slopes    : device fp32 [Hq], or NULL.
+ *   out       : device [total_new][Hq][D] in out_dtype; lse_out: device fp32
+ *               [total_new][Hq] natural log-sum-exp, or NULL.
+ *   workspace : device, 256-byte aligned; needs no initialisation, holds
+ *               nothing between calls.  Calls that may overlap on the GPU
+ *               (two streams, two graphs) need one each.
+ * A token that sees nothing gets a zero output and lse -inf.  What a token
+ * does not see never reaches its output, whatever the pool holds there.
+ * Scores are fp32 sums of exact products of codes and q (q in fp32: to 22
+ * bits); softmax statistics are fp32; the weights meet the values in fp16
+ * (11 bits) for a bf16 output and as two fp16 terms (22 bits) for fp32.
+ * Launches one kernel, or two when long contexts are split.
+ */
+LOOPVQ_API loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
+                                        const void* poolK, const void* poolV, const void* q, loopvq_dtype q_dtype,
+                                        int64_t q_stride_n, int64_t q_stride_h, const uint64_t* tree_mask,
+                                        int32_t loop_step, float softmax_scale, float softcap, const float* slopes,
+                                        void* out, loopvq_dtype out_dtype, float* lse_out, void* workspace,
+                                        size_t workspace_bytes, uint32_t* fault_bits, loopvq_stream_t stream);
+
+/*
+ * Keeps accepted drafts: with P = ctx_len - n_r (n_r <= 64), moves the codes
+ * of token P + keep[r][i] to P + i for i < n_keep[r], all loop steps, K and
+ * V.  The caller then sets the context to P + n_keep[r].
+ *   keep   : device int32 [batch][max_keep], indices in [0, n_r), any order.
+ *            An index out of range sets CTX_RANGE and its token keeps its bytes.
+ *   n_keep : device int32 [batch], 0 <= n_keep[r] <= min(n_r, max_keep) (else
+ *            CTX_RANGE and the request is left out).
+ */
+LOOPVQ_API loopvq_status loopvq_mx_keep(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
+                                        const int32_t* keep, const int32_t* n_keep, int32_t max_keep, void* poolK,
+                                        void* poolV, uint32_t* fault_bits, loopvq_stream_t stream);
+
 /* -------------------------------------------------- dense bf16 comparator */
 
 /* Workspace bytes of loopvq_dense_decode_attn. */

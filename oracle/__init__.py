@@ -11,3 +11,4 @@ Only the test-suite, ``__graft_entry__.smoke()`` and the ``cpu_baseline`` /
 (the C-ABI library and its Python binding) never calls it.
 """
 from .loopvq_oracle import *  # noqa: F401,F403
+from .mx_oracle import *

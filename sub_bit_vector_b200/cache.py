@@ -348,3 +348,179 @@ class PagedCache:
             out[:, :, p:p + n] = t.cpu().numpy()
             p += n
         return out
+
+
+class MXCache:
+    """Microscaled serving cache of one layer (K and V) for a batch of requests.
+
+    Every token is coded the moment it is written (``loopvq_mx_write``): e4m3
+    or e2m1 elements, one power-of-two scale per 32 channels, no codebook and
+    no window.  Contexts live in pages of ``page_tokens`` tokens, taken from a
+    free list.  A step:
+
+        cache.extend([1, 0, 7, ...])          # new tokens of each request
+        for t in range(n_loop):
+            cache.write(k_t, v_t, t)          # [rows][H][D], packed by request
+            out, lse = cache.attend(t, q_t, tree_mask)
+        cache.keep([None, [], [0, 2, 5], ...])  # trees: the accepted nodes
+
+    ``keep`` moves the accepted tokens behind the prefix and drops the rest;
+    ``truncate`` drops tokens at the end, ``read`` gives a range's values back.
+    Every request's lengths are host state; device arrays are made anew by each
+    ``extend``, so calls that are still running on the GPU keep theirs.  All
+    calls go to torch's current stream; a caller that changes streams orders
+    them as for any tensor.
+    """
+
+    def __init__(self, *, n_loop, n_heads_kv, head_dim, batch, max_ctx_len, format="e4m3", page_tokens=256,
+                 n_pages=None, n_heads_q=None, out_dtype=torch.bfloat16, device="cuda"):
+        if format not in ("e4m3", "e2m1"):
+            raise ValueError(f"unknown element format {format!r}")
+        if page_tokens < 32 or page_tokens % 32:
+            raise ValueError("page_tokens must be a positive multiple of 32")
+        self.device = torch.device(device)
+        self.T, self.H, self.D = n_loop, n_heads_kv, head_dim
+        self.Hq = n_heads_q or n_heads_kv
+        self.batch, self.max_ctx_len, self.page_tokens = batch, max_ctx_len, page_tokens
+        self.out_dtype = out_dtype
+        self.max_pages = max(1, -(-max_ctx_len // page_tokens))
+        self.n_pages = batch * self.max_pages if n_pages is None else n_pages
+        self.pool_tokens = self.n_pages * page_tokens
+        self.desc = L.make_mx_desc(n_loop, n_heads_kv, head_dim,
+                                   L.LOOPVQ_MX_E4M3 if format == "e4m3" else L.LOOPVQ_MX_E2M1, self.Hq)
+        nbytes = L.loopvq_mx_pool_bytes(self.desc, self.pool_tokens)
+        if nbytes == 0:
+            raise ValueError("invalid cache geometry")
+        self.poolK = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        self.poolV = torch.zeros_like(self.poolK)
+        self.fault_bits = torch.zeros(1, dtype=torch.int32, device=self.device)
+        self.ctx = [0] * batch
+        self.pages = [[] for _ in range(batch)]
+        self.free = list(range(self.n_pages))[::-1]
+        self.new = [0] * batch
+        self.rows = 0
+        self.layout = None
+
+    def _layout(self, ctx, new):
+        off = [0]
+        for n in new:
+            off.append(off[-1] + n)
+        dev = dict(dtype=torch.int32, device=self.device)
+        table = [p + [-1] * (self.max_pages - len(p)) for p in self.pages]
+        return L.make_mx_layout(self.batch, self.page_tokens, self.max_pages, self.pool_tokens, self.max_ctx_len,
+                                max(new), off[-1], torch.tensor(ctx, **dev), torch.tensor(off, **dev),
+                                torch.tensor(table, **dev))
+
+    # -------------------------------------------------------------- lengths
+    def extend(self, n_new) -> None:
+        """Contexts grow by n_new[r] tokens: the rows of the calls up to the
+        next ``extend``, packed in the order of the requests."""
+        n_new = [int(n) for n in n_new]
+        if len(n_new) != self.batch or min(n_new) < 0:
+            raise ValueError("one count of new tokens per request")
+        grown = [c + n for c, n in zip(self.ctx, n_new)]
+        if max(grown) > self.max_ctx_len:
+            raise ValueError("a context would exceed max_ctx_len")
+        need = [-(-c // self.page_tokens) - len(p) for c, p in zip(grown, self.pages)]
+        if sum(need) > len(self.free):
+            raise RuntimeError("cache out of pages")
+        for r, n in enumerate(need):
+            self.pages[r] += [self.free.pop() for _ in range(n)]
+        self.ctx, self.new, self.rows = grown, n_new, sum(n_new)
+        self.layout = self._layout(self.ctx, self.new)
+
+    def truncate(self, r, ctx_len) -> None:
+        """Request r's context ends at ctx_len; its pages behind that are free
+        (0: the request is over).  Ends the present step."""
+        if not 0 <= ctx_len <= self.ctx[r]:
+            raise ValueError("truncate cannot grow a context")
+        self.ctx[r] = ctx_len
+        held = -(-ctx_len // self.page_tokens)
+        self.free += self.pages[r][held:][::-1]
+        self.pages[r] = self.pages[r][:held]
+        self._end_step()
+
+    def _end_step(self):
+        self.new, self.rows, self.layout = [0] * self.batch, 0, None
+
+    def _step(self):
+        if self.layout is None:
+            raise RuntimeError("extend() begins a step")
+        return self.layout
+
+    # -------------------------------------------------------------- the step
+    def _rows(self, x, heads, lead):
+        if tuple(x.shape) != (*lead, self.rows, heads, self.D) or x.stride(-1) != 1:
+            raise ValueError(f"expected {[*lead, self.rows, heads, self.D]} with consecutive channels, "
+                             f"got {list(x.shape)}")
+
+    def write(self, k, v, loop_step=None) -> None:
+        """Keys and values of the new tokens: [rows][H][D] at one loop step, or
+        [T][rows][H][D] of all."""
+        lay = self._step()
+        lead = (self.T,) if loop_step is None else ()
+        self._rows(k, self.H, lead)
+        self._rows(v, self.H, lead)
+        if k.stride() != v.stride():
+            v = v.contiguous()
+            k = k.contiguous()
+        first, n = (0, self.T) if loop_step is None else (loop_step, 1)
+        L.loopvq_mx_write(self.desc, lay, first, n, k, v, k.stride(0) if lead else 0, k.stride(-3), k.stride(-2),
+                          self.poolK, self.poolV, self.fault_bits)
+
+    def attend(self, loop_step, q, tree_mask=None, softmax_scale=None, softcap=0.0, slopes=None):
+        """Attention of the new tokens at loop_step: q [rows][Hq][D] -> (out
+        [rows][Hq][D], lse [rows][Hq]).  tree_mask: int64 [rows], bit j of a
+        request's row i: its new token i sees its new token j (None: a chain)."""
+        lay = self._step()
+        self._rows(q, self.Hq, ())
+        out = torch.empty((self.rows, self.Hq, self.D), dtype=self.out_dtype, device=self.device)
+        lse = torch.empty((self.rows, self.Hq), dtype=torch.float32, device=self.device)
+        ws = torch.empty(max(256, L.loopvq_mx_attn_workspace_bytes(self.desc, lay)), dtype=torch.uint8,
+                         device=self.device)
+        L.loopvq_mx_attn(self.desc, lay, self.poolK, self.poolV, q, q.stride(0), q.stride(1), tree_mask, loop_step,
+                         self.D ** -0.5 if softmax_scale is None else softmax_scale, softcap, slopes, out, lse, ws,
+                         self.fault_bits)
+        return out, lse
+
+    def keep(self, accepted) -> None:
+        """accepted[r]: the new tokens of request r that stay, in the order
+        that they take behind the prefix (None: all of them as they are).
+        Ends the step."""
+        lay = self._step()
+        if len(accepted) != self.batch:
+            raise ValueError("one list of accepted tokens per request")
+        lists = [list(range(n)) if a is None else [int(i) for i in a] for a, n in zip(accepted, self.new)]
+        for a, n in zip(lists, self.new):
+            if len(a) > n or any(not 0 <= i < n for i in a):
+                raise ValueError("accepted tokens are indices of the request's new tokens")
+        if any(a != list(range(len(a))) for a in lists):   # else nothing moves
+            wide = max(len(a) for a in lists)
+            dev = dict(dtype=torch.int32, device=self.device)
+            L.loopvq_mx_keep(self.desc, lay, torch.tensor([a + [-1] * (wide - len(a)) for a in lists], **dev),
+                             torch.tensor([len(a) for a in lists], **dev), wide, self.poolK, self.poolV,
+                             self.fault_bits)
+        ends = [c - n + len(a) for c, n, a in zip(self.ctx, self.new, lists)]
+        for r, e in enumerate(ends):
+            self.truncate(r, e)
+        self._end_step()
+
+    def read(self, r, begin=0, end=None, first_step=0, n_steps=None, dtype=None):
+        """Values of tokens begin..end-1 of request r: (k, v), each [n_steps][tokens][H][D]."""
+        end = self.ctx[r] if end is None else end
+        n_steps = self.T - first_step if n_steps is None else n_steps
+        if not 0 <= begin <= end <= self.ctx[r]:
+            raise ValueError("the range is not in the context")
+        n = end - begin
+        lay = self._layout([end if i == r else 0 for i in range(self.batch)],
+                           [n if i == r else 0 for i in range(self.batch)])
+        k = torch.empty((n_steps, n, self.H, self.D), dtype=dtype or self.out_dtype, device=self.device)
+        v = torch.empty_like(k)
+        if n:
+            L.loopvq_mx_read(self.desc, lay, first_step, n_steps, self.poolK, self.poolV, k, v, n * self.H * self.D,
+                             self.H * self.D, self.D, self.fault_bits)
+        return k, v
+
+    def device_faults(self) -> int:
+        """LOOPVQ_FAULT_* bits that the calls so far have set; waits for them."""
+        return int(self.fault_bits.item())

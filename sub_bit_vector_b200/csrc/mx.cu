@@ -1,0 +1,683 @@
+// Microscaled KV cache: quantise as written, read back, keep accepted drafts.
+//
+// A block of 32 channels of one token shares the scale 2^e, e the least
+// integer in [-64, 56] with max|x| <= top * 2^e; a code is the element value
+// nearest to x * 2^-e.  Scaling by a power of two is exact, so the one
+// rounding is the conversion instruction's (nearest even).
+//
+// All three kernels move bytes; DRAM bounds them.  A warp owns one tile (32
+// tokens) of one head of K or V, because a tile's bytes interleave its tokens
+// the way the attention's matrix instructions take them: the lane that loads
+// a piece of a row in the order of the pool is the lane that stores it, in
+// 16-byte pieces, with no exchange but the block's maximum.  The warps of a
+// CTA take neighbouring heads, whose rows are neighbours in x.
+#include "mx.cuh"
+
+namespace loopvq {
+namespace {
+
+struct MxMoveParams {
+  MxLayout L;
+  int H, n_steps, first_step, head_groups;
+  int64_t st, sn, sh;
+  const void *xk, *xv;   // write: in
+  void *ok, *ov;         // read: out
+  uint8_t *pk, *pv;
+  uint32_t* fault;
+};
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// Scale byte of a block with largest magnitude bits m, and 2^-e.
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_scale(uint32_t m, float* inv) {
+  // top = 1.75 * 2^8 or 1.5 * 2^2: e = exponent - 8 (2), one more above top's fraction
+  constexpr int kTopExp = FMT == LOOPVQ_MX_E4M3 ? 8 : 2;
+  constexpr uint32_t kTopFrac = FMT == LOOPVQ_MX_E4M3 ? 0x600000u : 0x400000u;
+  int e = (int)(m >> 23) - 127 - kTopExp + ((m & 0x7fffffu) > kTopFrac ? 1 : 0);
+  e = max(kMxExpMin, min(kMxExpMax, e));
+  *inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  return m >= 0x7f800000u ? kMxNan : (uint32_t)(e + 127);
+}
+// Four scaled values to codes: e4m3 in the 4 bytes, e2m1 in the low 4 nibbles.
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_codes4(float a, float b, float c, float d) {
+  if constexpr (FMT == LOOPVQ_MX_E4M3) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)lo | (uint32_t)hi << 16;
+  } else {
+    uint16_t r;
+    asm("{\n .reg .b8 p0, p1;\n cvt.rn.satfinite.e2m1x2.f32 p0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 p1, %4, %3;\n"
+        " mov.b16 %0, {p0, p1};\n}"
+        : "=h"(r)
+        : "f"(a), "f"(b), "f"(c), "f"(d));
+    return r;
+  }
+}
+
+// N consecutive channels of x; vector loads when VEC.
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void load_channels(const T* p, float* v) {
+  if constexpr (VEC && sizeof(T) == 2) {
+    uint32_t w[N / 2];
+    if constexpr (N == 8) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    } else {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = u.x; w[1] = u.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
+      v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = to_f32<T>(p[i]);
+  }
+}
+template <typename T, int N, bool VEC>
+__device__ __forceinline__ void store_channels(T* p, const float* v) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if constexpr (VEC && N == 8) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (VEC) {
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      if constexpr (VEC)
+        reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      else
+        for (int j = 0; j < 4; ++j) p[4 * i + j] = v[4 * i + j];
+    }
+  }
+}
+
+// What a warp of the write and read kernels works on.
+struct MxUnit {
+  MxReq q;
+  int tok0;        // first token of the tile
+  int kind, h, s;  // K or V, head, step - first_step
+  uint8_t* tile;
+};
+// The unit of this warp, or false if it has none.
+template <int D, int FMT>
+__device__ __forceinline__ bool mx_unit(const MxMoveParams& p, MxUnit* u) {
+  const int hg = blockIdx.x % p.head_groups, tile_i = blockIdx.x / p.head_groups;
+  const int hk = hg * 8 + (threadIdx.x >> 5);
+  if (hk >= 2 * p.H) return false;
+  const int r = blockIdx.z;
+  if (!mx_request(p.L, r, &u->q, p.fault)) return false;
+  const int t = u->q.base / kMxTile + tile_i;
+  u->tok0 = t * kMxTile;
+  if (u->q.n == 0 || u->tok0 >= u->q.ctx) return false;
+  const int64_t pt = mx_pool_tile(p.L, r, t, p.fault);
+  if (pt < 0) return false;
+  u->kind = hk >= p.H;
+  u->h = hk - u->kind * p.H;
+  u->s = blockIdx.y;
+  u->tile = (u->kind ? p.pv : p.pk) +
+            (((int64_t)(p.first_step + u->s) * p.H + u->h) * p.L.pool_tiles + pt) * MxTile<D, FMT>::kBytes;
+  return true;
+}
+
+// Quantise: K lanes hold 8 channels of two tokens per block, V lanes 4
+// channels of four tokens.
+template <int D, int FMT, typename T, bool VEC>
+__global__ void __launch_bounds__(256) mx_write_kernel(const MxMoveParams p) {
+  using Tile = MxTile<D, FMT>;
+  constexpr int NB = Tile::kBlocks;
+  MxUnit u;
+  if (!mx_unit<D, FMT>(p, &u)) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const T* x = reinterpret_cast<const T*>(u.kind ? p.xv : p.xk) + u.s * p.st + u.h * p.sh +
+               (int64_t)u.q.row0 * p.sn;
+#pragma unroll 1
+  for (int sub = 0; sub < 2; ++sub) {
+    const int first = u.tok0 + 16 * sub;
+    if (first + 16 <= u.q.base || first >= u.q.ctx) continue;
+    if (u.kind == LOOPVQ_KEYS) {
+      const int tok[2] = {first + 4 * (g >> 1) + (g & 1), first + 4 * (g >> 1) + (g & 1) + 2};
+      const bool in[2] = {tok[0] >= u.q.base && tok[0] < u.q.ctx, tok[1] >= u.q.base && tok[1] < u.q.ctx};
+      float v[2][NB][8];
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if (in[a])
+            load_channels<T, 8, VEC>(x + (int64_t)(tok[a] - u.q.base) * p.sn + 32 * b + 8 * c, v[a][b]);
+          else
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[a][b][i] = 0.f;
+        }
+      uint32_t sc[2] = {0, 0}, lo[2][NB], hi[2][NB];
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[a][b][i]));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          float inv;
+          const uint32_t byte = mx_scale<FMT>(m, &inv);
+          sc[a] |= byte << (8 * b);
+          float* w = v[a][b];
+          const bool fin = byte != kMxNan;
+          lo[a][b] = fin ? mx_codes4<FMT>(w[0] * inv, w[1] * inv, w[2] * inv, w[3] * inv) : 0u;
+          hi[a][b] = fin ? mx_codes4<FMT>(w[4] * inv, w[5] * inv, w[6] * inv, w[7] * inv) : 0u;
+          if constexpr (FMT == LOOPVQ_MX_E2M1) lo[a][b] |= hi[a][b] << 16;
+        }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint8_t* d = u.tile + mx_code_off<D, FMT>(sub, b, lane);
+        if constexpr (FMT == LOOPVQ_MX_E4M3) {
+          if (in[0] && in[1]) {
+            *reinterpret_cast<uint4*>(d) = make_uint4(lo[0][b], hi[0][b], lo[1][b], hi[1][b]);
+          } else {
+            if (in[0]) *reinterpret_cast<uint2*>(d) = make_uint2(lo[0][b], hi[0][b]);
+            if (in[1]) *reinterpret_cast<uint2*>(d + 8) = make_uint2(lo[1][b], hi[1][b]);
+          }
+        } else {
+          if (in[0] && in[1]) {
+            if ((b & 1) == 0)
+              *reinterpret_cast<uint4*>(d) = make_uint4(lo[0][b], lo[1][b], lo[0][b + 1], lo[1][b + 1]);
+          } else {
+            if (in[0]) *reinterpret_cast<uint32_t*>(d) = lo[0][b];
+            if (in[1]) *reinterpret_cast<uint32_t*>(d + 4) = lo[1][b];
+          }
+        }
+      }
+      // lane c stores the scales of block c
+      if (c < NB) {
+        uint8_t* d = u.tile + mx_scale_off<D, FMT>(sub * 4 + (g >> 1), c) + (g & 1);
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+          if (in[a]) d[2 * a] = (uint8_t)(sc[a] >> (8 * c));
+      }
+    } else {
+      const int tok = first + 4 * c;
+      uint32_t in_mask = 0;   // a byte per new token of the quad
+      float v[4][NB][4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const bool in = tok + t >= u.q.base && tok + t < u.q.ctx;
+        in_mask |= in ? 0xffu << (8 * t) : 0u;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if (in)
+            load_channels<T, 4, VEC>(x + (int64_t)(tok + t - u.q.base) * p.sn + 32 * b + 4 * g, v[t][b]);
+          else
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[t][b][i] = 0.f;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t sc = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[t][b][i]));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
+          float inv;
+          const uint32_t byte = mx_scale<FMT>(m, &inv);
+          sc |= byte << (8 * t);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[t][b][i] = byte != kMxNan ? v[t][b][i] * inv : 0.f;
+        }
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = mx_codes4<FMT>(v[0][b][j], v[1][b][j], v[2][b][j], v[3][b][j]);
+        uint8_t* d = u.tile + mx_code_off<D, FMT>(sub, b, lane);
+        uint32_t* ds = reinterpret_cast<uint32_t*>(u.tile + mx_scale_off<D, FMT>(sub * 4 + c, b));
+        if (in_mask == 0) continue;
+        // the quad's old tokens keep their bits
+        if constexpr (FMT == LOOPVQ_MX_E4M3) {
+          uint4 o = make_uint4(w[0], w[1], w[2], w[3]);
+          if (in_mask != 0xffffffffu) {
+            const uint4 old = *reinterpret_cast<const uint4*>(d);
+            o.x = (o.x & in_mask) | (old.x & ~in_mask);
+            o.y = (o.y & in_mask) | (old.y & ~in_mask);
+            o.z = (o.z & in_mask) | (old.z & ~in_mask);
+            o.w = (o.w & in_mask) | (old.w & ~in_mask);
+          }
+          *reinterpret_cast<uint4*>(d) = o;
+        } else {
+          uint2 o = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+          if (in_mask != 0xffffffffu) {
+            uint32_t nm = 0;   // a nibble per token, twice
+#pragma unroll
+            for (int t = 0; t < 4; ++t) nm |= (in_mask >> (8 * t) & 1u) ? 0x000f000fu << (4 * t) : 0u;
+            const uint2 old = *reinterpret_cast<const uint2*>(d);
+            o.x = (o.x & nm) | (old.x & ~nm);
+            o.y = (o.y & nm) | (old.y & ~nm);
+          }
+          *reinterpret_cast<uint2*>(d) = o;
+        }
+        if (g == 0) *ds = in_mask == 0xffffffffu ? sc : (sc & in_mask) | (*ds & ~in_mask);
+      }
+    }
+  }
+}
+
+// Codes to values.
+template <int FMT>
+__device__ __forceinline__ float2 mx_value2(uint32_t code2) {  // two codes in the low 16 or 8 bits
+  uint32_t h;
+  if constexpr (FMT == LOOPVQ_MX_E4M3)
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)code2));
+  else
+    asm("{\n .reg .b8 a, z1, z2, z3;\n mov.b32 {a, z1, z2, z3}, %1;\n cvt.rn.f16x2.e2m1x2 %0, a;\n}" : "=r"(h) : "r"(code2));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float mx_scale_value(uint32_t byte) {
+  // 2^(byte - 127); byte 0 is the subnormal 2^-127, 255 is NaN
+  return __uint_as_float(byte == kMxNan ? 0x7fffffffu : byte == 0 ? 0x00400000u : byte << 23);
+}
+
+template <int D, int FMT, typename T, bool VEC>
+__global__ void __launch_bounds__(256) mx_read_kernel(const MxMoveParams p) {
+  using Tile = MxTile<D, FMT>;
+  constexpr int NB = Tile::kBlocks;
+  MxUnit u;
+  if (!mx_unit<D, FMT>(p, &u)) return;
+  const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  T* x = reinterpret_cast<T*>(u.kind ? p.ov : p.ok) + u.s * p.st + u.h * p.sh + (int64_t)u.q.row0 * p.sn;
+#pragma unroll 1
+  for (int sub = 0; sub < 2; ++sub) {
+    const int first = u.tok0 + 16 * sub;
+    if (first + 16 <= u.q.base || first >= u.q.ctx) continue;
+    // the half tile's codes and scales of this lane
+    uint32_t w[NB][Tile::kLaneBytes / 4], sw[NB];
+    if constexpr (FMT == LOOPVQ_MX_E4M3) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint4 z = __ldg(reinterpret_cast<const uint4*>(u.tile + mx_code_off<D, FMT>(sub, b, lane)));
+        w[b][0] = z.x; w[b][1] = z.y; w[b][2] = z.z; w[b][3] = z.w;
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < NB; b += 2) {
+        const uint4 z = __ldg(reinterpret_cast<const uint4*>(u.tile + mx_code_off<D, FMT>(sub, b, lane)));
+        w[b][0] = z.x; w[b][1] = z.y; w[b + 1][0] = z.z; w[b + 1][1] = z.w;
+      }
+    }
+    if (u.kind == LOOPVQ_KEYS) {
+#pragma unroll
+      for (int a = 0; a < 2; ++a) {
+        const int tok = first + 4 * (g >> 1) + (g & 1) + 2 * a;
+        if (tok < u.q.base || tok >= u.q.ctx) continue;
+        T* row = x + (int64_t)(tok - u.q.base) * p.sn;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float s = mx_scale_value(u.tile[mx_scale_off<D, FMT>(sub * 4 + (g >> 1), b) + (g & 1) + 2 * a]);
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = FMT == LOOPVQ_MX_E4M3 ? mx_value2<FMT>(w[b][2 * a + (i >> 1)] >> (16 * (i & 1)))
+                                                   : mx_value2<FMT>(w[b][a] >> (8 * i));
+            v[2 * i] = f.x * s;
+            v[2 * i + 1] = f.y * s;
+          }
+          store_channels<T, 8, VEC>(row + 32 * b + 8 * c, v);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        sw[b] = *reinterpret_cast<const uint32_t*>(u.tile + mx_scale_off<D, FMT>(sub * 4 + c, b));
+#pragma unroll
+      for (int t2 = 0; t2 < 2; ++t2)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float v[2][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = FMT == LOOPVQ_MX_E4M3 ? mx_value2<FMT>(w[b][j] >> (16 * t2))
+                                                   : mx_value2<FMT>(w[b][j >> 1] >> (16 * (j & 1) + 8 * t2));
+            v[0][j] = f.x;
+            v[1][j] = f.y;
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int tok = first + 4 * c + 2 * t2 + t;
+            if (tok < u.q.base || tok >= u.q.ctx) continue;
+            const float s = mx_scale_value(sw[b] >> (8 * (2 * t2 + t)) & 255u);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[t][j] *= s;
+            store_channels<T, 4, VEC>(x + (int64_t)(tok - u.q.base) * p.sn + 32 * b + 4 * g, v[t]);
+          }
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------------- keep
+//
+// A warp owns one head of K or V of one step of one request.  It takes the
+// (at most three) tiles that hold the request's new tokens into shared
+// memory, and only then writes the moved tokens from that copy: any order
+// of indices is safe, nothing is read after it was overwritten.
+constexpr int kMxKeepTiles = (kMxMaxTree + kMxTile - 2) / kMxTile + 1;
+constexpr int kMxKeepWarps = 4;
+
+struct MxKeepParams {
+  MxLayout L;
+  int H;
+  const int32_t *keep, *n_keep;
+  int max_keep;
+  uint8_t *pk, *pv;
+  uint32_t* fault;
+};
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeepParams p) {
+  using Tile = MxTile<D, FMT>;
+  constexpr int NB = Tile::kBlocks;
+  extern __shared__ __align__(16) uint8_t sm_all[];
+  __shared__ int16_t sm_src[kMxKeepWarps][kMxKeepTiles * kMxTile];   // by token - 32 * first tile
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* sm = sm_all + warp * kMxKeepTiles * Tile::kBytes;
+  int16_t* src = sm_src[warp];
+  const int hk = blockIdx.x * kMxKeepWarps + warp;
+  if (hk >= 2 * p.H) return;
+  const int r = blockIdx.z;
+  MxReq q;
+  if (!mx_request(p.L, r, &q, p.fault)) return;
+  const int nk = __ldg(p.n_keep + r);
+  if (nk < 0 || nk > q.n || nk > p.max_keep) {
+    set_fault(p.fault, LOOPVQ_FAULT_CTX_RANGE);
+    return;
+  }
+  if (nk == 0) return;
+  const int t0 = q.base / kMxTile, org = t0 * kMxTile;
+  const int n_tiles = (q.ctx - 1) / kMxTile - t0 + 1;   // n <= 64: at most kMxKeepTiles
+  const int kind = hk >= p.H, h = hk - kind * p.H;
+  uint8_t* stream = (kind ? p.pv : p.pk) + ((int64_t)blockIdx.y * p.H + h) * p.L.pool_tiles * Tile::kBytes;
+  int64_t tile_at[kMxKeepTiles];
+#pragma unroll
+  for (int i = 0; i < kMxKeepTiles; ++i) {
+    tile_at[i] = i < n_tiles ? mx_pool_tile(p.L, r, t0 + i, p.fault) : -1;
+    if (tile_at[i] >= 0) {
+      const uint4* s = reinterpret_cast<const uint4*>(stream + tile_at[i] * Tile::kBytes);
+      for (int b = lane; b < Tile::kBytes / 16; b += 32) reinterpret_cast<uint4*>(sm + i * Tile::kBytes)[b] = s[b];
+    }
+  }
+  // where each token of these tiles comes from (-1: it stays)
+  for (int i = lane; i < kMxKeepTiles * kMxTile; i += 32) {
+    const int k = org + i - q.base;
+    int from = -1;
+    if (k >= 0 && k < nk) {
+      const int f = __ldg(p.keep + (int64_t)r * p.max_keep + k);
+      if (f < 0 || f >= q.n) {
+        set_fault(p.fault, LOOPVQ_FAULT_CTX_RANGE);
+      } else if (f != k) {
+        from = q.base + f - org;
+        if (mx_pool_tile(p.L, r, t0 + from / kMxTile, p.fault) < 0) from = -1;
+      }
+    }
+    src[i] = (int16_t)from;
+  }
+  __syncwarp();
+  const int last = q.base + nk - 1 - org;   // last token written
+#pragma unroll
+  for (int i = 0; i < kMxKeepTiles; ++i) {
+    if (tile_at[i] < 0 || i * kMxTile > last) continue;
+    uint8_t* out = stream + tile_at[i] * Tile::kBytes;
+    if (kind == LOOPVQ_KEYS) {
+      // a piece: 8 channels of one token (8 or 4 bytes)
+      constexpr int kPiece = Tile::kLaneBytes / 2;
+      for (int e = lane; e < kMxTile * NB * 4; e += 32) {
+        const int cc = e & 3, b = (e >> 2) % NB, n = e / (4 * NB), f = src[i * kMxTile + n];
+        if (f < 0) continue;
+        auto off = [&](int m) {
+          const int gg = ((m & 15) >> 2) * 2 + (m & 1), ab = m >> 1 & 1;
+          return mx_code_off<D, FMT>(m >> 4 & 1, b, gg * 4 + cc) + ab * kPiece;
+        };
+        const uint8_t* s = sm + (f / kMxTile) * Tile::kBytes + off(f % kMxTile);
+        uint8_t* d = out + off(n);
+        if constexpr (kPiece == 8) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(s);
+        else *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(s);
+      }
+    } else {
+      // a word: four tokens of one channel (e4m3) or of two (e2m1); the tokens
+      // that stay keep their bits, which this warp alone may write
+      constexpr int kWords = Tile::kLaneBytes / 4;   // of a lane and block
+      for (int e = lane; e < 8 * NB * 8 * kWords; e += 32) {
+        const int j = e % kWords, gg = e / kWords % 8, b = e / (kWords * 8) % NB, quad = e / (kWords * 8 * NB);
+        auto off = [&](int m) { return mx_code_off<D, FMT>(m >> 4 & 1, b, gg * 4 + (m >> 2 & 3)) + j * 4; };
+        const int16_t* qs = src + i * kMxTile + quad * 4;
+        uint32_t mask = 0, bits = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int f = qs[t];
+          if (f < 0) continue;
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(sm + (f / kMxTile) * Tile::kBytes + off(f % kMxTile));
+          if constexpr (FMT == LOOPVQ_MX_E4M3) {
+            mask |= 0xffu << (8 * t);
+            bits |= (w >> (8 * (f & 3)) & 0xffu) << (8 * t);
+          } else {
+            mask |= 0x000f000fu << (4 * t);
+            bits |= (w >> (4 * (f & 3)) & 0x000f000fu) << (4 * t);
+          }
+        }
+        if (mask) {
+          const uint32_t old = *reinterpret_cast<const uint32_t*>(sm + i * Tile::kBytes + off(quad * 4));
+          *reinterpret_cast<uint32_t*>(out + off(quad * 4)) = (old & ~mask) | bits;
+        }
+      }
+    }
+    for (int e = lane; e < 8 * NB; e += 32) {   // scale words: four tokens of one block
+      const int b = e % NB, quad = e / NB;
+      const uint32_t old = *reinterpret_cast<const uint32_t*>(sm + i * Tile::kBytes + mx_scale_off<D, FMT>(quad, b));
+      uint32_t now = old;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int f = src[i * kMxTile + quad * 4 + t];
+        if (f < 0) continue;
+        const int at = (f / kMxTile) * Tile::kBytes + mx_scale_off<D, FMT>(f % kMxTile >> 2, b);
+        now = (now & ~(0xffu << (8 * t))) | (uint32_t)sm[at + (f & 3)] << (8 * t);
+      }
+      if (now != old) *reinterpret_cast<uint32_t*>(out + mx_scale_off<D, FMT>(quad, b)) = now;
+    }
+  }
+}
+
+loopvq_status move_setup(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout, int32_t first_step,
+                         int32_t n_steps, loopvq_dtype dtype, int64_t st, int64_t sn, int64_t sh, const void* poolK,
+                         const void* poolV, uint32_t* fault, MxMoveParams* p, dim3* grid) {
+  loopvq_status s = mx_check_desc(desc);
+  if (s != LOOPVQ_OK) return s;
+  s = mx_check_layout(layout, &p->L);
+  if (s != LOOPVQ_OK) return s;
+  if (first_step < 0 || n_steps < 1 || n_steps > desc->n_loop - first_step) return LOOPVQ_ERR_INVALID_ARG;
+  if (dtype != LOOPVQ_F32 && dtype != LOOPVQ_BF16) return LOOPVQ_ERR_INVALID_ARG;
+  if (st < 0 || sn < 0 || sh < 0) return LOOPVQ_ERR_INVALID_ARG;
+  if (!poolK || !poolV || ((uintptr_t)poolK & 15) || ((uintptr_t)poolV & 15) || ((uintptr_t)fault & 3))
+    return LOOPVQ_ERR_INVALID_ARG;
+  p->H = desc->n_heads_kv;
+  p->n_steps = n_steps;
+  p->first_step = first_step;
+  p->head_groups = (2 * p->H + 7) / 8;
+  p->st = st; p->sn = sn; p->sh = sh;
+  p->pk = (uint8_t*)poolK;
+  p->pv = (uint8_t*)poolV;
+  p->fault = fault;
+  // tiles that a request's new tokens can touch
+  int64_t tiles = ((int64_t)p->L.max_new + kMxTile - 2) / kMxTile + 1;
+  const int64_t all = ((int64_t)p->L.max_ctx + kMxTile - 1) / kMxTile;
+  if (tiles > all) tiles = all;
+  const int64_t x = tiles * p->head_groups;
+  if (x > 0x7fffffffLL || n_steps > 65535) return LOOPVQ_ERR_UNSUPPORTED;
+  *grid = dim3((unsigned)x, (unsigned)n_steps, (unsigned)p->L.batch);
+  return LOOPVQ_OK;
+}
+// Vector loads and stores of 8 bf16 or 4 fp32 channels.
+bool vec_ok(const void* a, const void* b, size_t es, const MxMoveParams& p) {
+  const uint64_t m = (uint64_t)(uintptr_t)a | (uint64_t)(uintptr_t)b | (uint64_t)p.st * es | (uint64_t)p.sn * es |
+                     (uint64_t)p.sh * es;
+  return (m & 15) == 0;
+}
+
+}  // namespace
+
+loopvq_status mx_check_desc(const loopvq_mx_desc* d) {
+  if (!d || d->n_loop < 1 || d->n_heads_kv < 1 || d->n_heads_q < 1 || d->head_dim < 1) return LOOPVQ_ERR_INVALID_ARG;
+  if (d->n_heads_q % d->n_heads_kv) return LOOPVQ_ERR_INVALID_ARG;
+  if (d->format != LOOPVQ_MX_E4M3 && d->format != LOOPVQ_MX_E2M1) return LOOPVQ_ERR_INVALID_ARG;
+  if (d->head_dim != 64 && d->head_dim != 128) return LOOPVQ_ERR_UNSUPPORTED;
+  if (d->n_heads_kv > 65535 || d->n_heads_q > 65535) return LOOPVQ_ERR_UNSUPPORTED;
+  return LOOPVQ_OK;
+}
+
+loopvq_status mx_check_layout(const loopvq_mx_layout* l, MxLayout* o) {
+  if (!l || l->batch < 1 || l->batch > 65535 || l->page_tokens < kMxTile || l->page_tokens % kMxTile ||
+      l->max_pages < 1 || l->max_ctx_len < 0 || l->max_new < 0 || l->total_new < 0 || l->pool_tokens < kMxTile ||
+      l->pool_tokens % kMxTile)
+    return LOOPVQ_ERR_INVALID_ARG;
+  if (l->max_ctx_len > (int64_t)l->max_pages * l->page_tokens) return LOOPVQ_ERR_INVALID_ARG;
+  if (!l->pages || !l->ctx_len || !l->new_off) return LOOPVQ_ERR_INVALID_ARG;
+  if (((uintptr_t)l->pages | (uintptr_t)l->ctx_len | (uintptr_t)l->new_off) & 3) return LOOPVQ_ERR_INVALID_ARG;
+  o->batch = l->batch;
+  o->page_tokens = l->page_tokens;
+  o->max_pages = l->max_pages;
+  o->max_ctx = l->max_ctx_len;
+  o->max_new = l->max_new;
+  o->total_new = l->total_new;
+  o->n_pages = l->pool_tokens / l->page_tokens;
+  o->pool_tiles = l->pool_tokens / kMxTile;
+  o->pages = l->pages;
+  o->ctx_len = l->ctx_len;
+  o->new_off = l->new_off;
+  return LOOPVQ_OK;
+}
+
+}  // namespace loopvq
+
+using namespace loopvq;
+
+#define MX_BY_TYPE(KERNEL, GRID, STREAM, P, T, V)                                                     \
+  do {                                                                                                \
+    if (desc->head_dim == 128) {                                                                      \
+      if (desc->format == LOOPVQ_MX_E4M3) KERNEL<128, LOOPVQ_MX_E4M3, T, V><<<GRID, 256, 0, STREAM>>>(P); \
+      else KERNEL<128, LOOPVQ_MX_E2M1, T, V><<<GRID, 256, 0, STREAM>>>(P);                             \
+    } else {                                                                                          \
+      if (desc->format == LOOPVQ_MX_E4M3) KERNEL<64, LOOPVQ_MX_E4M3, T, V><<<GRID, 256, 0, STREAM>>>(P);  \
+      else KERNEL<64, LOOPVQ_MX_E2M1, T, V><<<GRID, 256, 0, STREAM>>>(P);                              \
+    }                                                                                                 \
+  } while (0)
+#define MX_MOVE(KERNEL, DTYPE, A, B)                                                   \
+  do {                                                                                 \
+    if (DTYPE == LOOPVQ_BF16) {                                                        \
+      if (vec_ok(A, B, 2, p)) MX_BY_TYPE(KERNEL, grid, (cudaStream_t)stream, p, __nv_bfloat16, true);  \
+      else MX_BY_TYPE(KERNEL, grid, (cudaStream_t)stream, p, __nv_bfloat16, false);    \
+    } else {                                                                           \
+      if (vec_ok(A, B, 4, p)) MX_BY_TYPE(KERNEL, grid, (cudaStream_t)stream, p, float, true);          \
+      else MX_BY_TYPE(KERNEL, grid, (cudaStream_t)stream, p, float, false);            \
+    }                                                                                  \
+  } while (0)
+
+extern "C" size_t loopvq_mx_pool_bytes(const loopvq_mx_desc* desc, int64_t pool_tokens) {
+  if (mx_check_desc(desc) != LOOPVQ_OK || pool_tokens < kMxTile || pool_tokens % kMxTile) return 0;
+  return (size_t)desc->n_loop * desc->n_heads_kv * (size_t)(pool_tokens / kMxTile) *
+         mx_tile_bytes(desc->head_dim, desc->format);
+}
+
+extern "C" loopvq_status loopvq_mx_write(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
+                                         int32_t first_step, int32_t n_steps, const void* k, const void* v,
+                                         loopvq_dtype x_dtype, int64_t stride_t, int64_t stride_n,
+                                         int64_t stride_h, void* poolK, void* poolV, uint32_t* fault_bits,
+                                         loopvq_stream_t stream) {
+  MxMoveParams p = {};
+  dim3 grid;
+  const loopvq_status st = move_setup(desc, layout, first_step, n_steps, x_dtype, stride_t, stride_n, stride_h,
+                                      poolK, poolV, fault_bits, &p, &grid);
+  if (st != LOOPVQ_OK) return st;
+  if (layout->total_new == 0 || layout->max_new == 0 || layout->max_ctx_len == 0) return LOOPVQ_OK;
+  const uintptr_t es = x_dtype == LOOPVQ_BF16 ? 2 : 4;
+  if (!k || !v || (uintptr_t)k % es || (uintptr_t)v % es) return LOOPVQ_ERR_INVALID_ARG;
+  p.xk = k;
+  p.xv = v;
+  MX_MOVE(mx_write_kernel, x_dtype, k, v);
+  return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+}
+
+extern "C" loopvq_status loopvq_mx_read(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
+                                        int32_t first_step, int32_t n_steps, const void* poolK, const void* poolV,
+                                        void* k_out, void* v_out, loopvq_dtype out_dtype, int64_t stride_t,
+                                        int64_t stride_n, int64_t stride_h, uint32_t* fault_bits,
+                                        loopvq_stream_t stream) {
+  MxMoveParams p = {};
+  dim3 grid;
+  const loopvq_status st = move_setup(desc, layout, first_step, n_steps, out_dtype, stride_t, stride_n, stride_h,
+                                      poolK, poolV, fault_bits, &p, &grid);
+  if (st != LOOPVQ_OK) return st;
+  if (layout->total_new == 0 || layout->max_new == 0 || layout->max_ctx_len == 0) return LOOPVQ_OK;
+  const uintptr_t es = out_dtype == LOOPVQ_BF16 ? 2 : 4;
+  if (!k_out || !v_out || (uintptr_t)k_out % es || (uintptr_t)v_out % es) return LOOPVQ_ERR_INVALID_ARG;
+  // rows, heads and steps must not meet in the output
+  if ((n_steps > 1 && stride_t == 0) || (layout->total_new > 1 && stride_n == 0) ||
+      (desc->n_heads_kv > 1 && stride_h == 0))
+    return LOOPVQ_ERR_INVALID_ARG;
+  p.ok = k_out;
+  p.ov = v_out;
+  MX_MOVE(mx_read_kernel, out_dtype, k_out, v_out);
+  return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+}
+
+extern "C" loopvq_status loopvq_mx_keep(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
+                                        const int32_t* keep, const int32_t* n_keep, int32_t max_keep, void* poolK,
+                                        void* poolV, uint32_t* fault_bits, loopvq_stream_t stream) {
+  MxKeepParams p = {};
+  loopvq_status st = mx_check_desc(desc);
+  if (st != LOOPVQ_OK) return st;
+  st = mx_check_layout(layout, &p.L);
+  if (st != LOOPVQ_OK) return st;
+  if (!keep || !n_keep || max_keep < 1 || ((uintptr_t)keep & 3) || ((uintptr_t)n_keep & 3)) return LOOPVQ_ERR_INVALID_ARG;
+  if (!poolK || !poolV || ((uintptr_t)poolK & 15) || ((uintptr_t)poolV & 15) || ((uintptr_t)fault_bits & 3))
+    return LOOPVQ_ERR_INVALID_ARG;
+  if (layout->max_new > kMxMaxTree || desc->n_loop > 65535) return LOOPVQ_ERR_UNSUPPORTED;
+  if (layout->total_new == 0 || layout->max_new == 0 || layout->max_ctx_len == 0) return LOOPVQ_OK;
+  p.H = desc->n_heads_kv;
+  p.keep = keep;
+  p.n_keep = n_keep;
+  p.max_keep = max_keep;
+  p.pk = (uint8_t*)poolK;
+  p.pv = (uint8_t*)poolV;
+  p.fault = fault_bits;
+  const dim3 grid((2 * p.H + kMxKeepWarps - 1) / kMxKeepWarps, desc->n_loop, p.L.batch);
+  const size_t smem = kMxKeepWarps * kMxKeepTiles * mx_tile_bytes(desc->head_dim, desc->format);
+  auto kfn = desc->head_dim == 128
+                 ? (desc->format == LOOPVQ_MX_E4M3 ? mx_keep_kernel<128, LOOPVQ_MX_E4M3> : mx_keep_kernel<128, LOOPVQ_MX_E2M1>)
+                 : (desc->format == LOOPVQ_MX_E4M3 ? mx_keep_kernel<64, LOOPVQ_MX_E4M3> : mx_keep_kernel<64, LOOPVQ_MX_E2M1>);
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    return LOOPVQ_ERR_CUDA;
+  kfn<<<grid, kMxKeepWarps * 32, smem, (cudaStream_t)stream>>>(p);
+  return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+}

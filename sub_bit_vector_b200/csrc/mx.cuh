@@ -1,0 +1,82 @@
+// Microscaled KV cache: tile layout, request and page lookup shared by the
+// kernels that write, read, move and attend over it.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace loopvq {
+
+constexpr int kMxTile = 32;    // tokens of a tile
+constexpr int kMxBlock = 32;   // channels that share a scale
+constexpr int kMxMaxTree = 64; // new tokens a request may have in attention and keep
+constexpr int kMxExpMin = -64, kMxExpMax = 56;
+constexpr uint32_t kMxNan = 255;
+
+// D channels, FMT element format: sizes of one tile.  A unit is 512 bytes,
+// 16 per lane: one block of 16 tokens for e4m3, two for e2m1.
+template <int D, int FMT>
+struct MxTile {
+  static constexpr int kBlocks = D / kMxBlock;
+  static constexpr int kLaneBytes = FMT == LOOPVQ_MX_E4M3 ? 16 : 8;  // of one block of one half tile
+  static constexpr int kHalfBytes = kBlocks * 32 * kLaneBytes;
+  static constexpr int kScaleOff = 2 * kHalfBytes;
+  static constexpr int kBytes = kScaleOff + kMxTile * kBlocks;
+};
+// Byte of lane `lane`'s codes of block b of half sub.
+template <int D, int FMT>
+__host__ __device__ constexpr int mx_code_off(int sub, int b, int lane) {
+  return FMT == LOOPVQ_MX_E4M3 ? sub * MxTile<D, FMT>::kHalfBytes + (b * 32 + lane) * 16
+                               : sub * MxTile<D, FMT>::kHalfBytes + ((b >> 1) * 32 + lane) * 16 + (b & 1) * 8;
+}
+// Byte of the scale word of block b for tokens 4 * quad .. 4 * quad + 3 of a tile.
+template <int D, int FMT>
+__host__ __device__ constexpr int mx_scale_off(int quad, int b) {
+  return MxTile<D, FMT>::kScaleOff + (quad * MxTile<D, FMT>::kBlocks + b) * 4;
+}
+inline size_t mx_tile_bytes(int D, int fmt) {
+  return (size_t)kMxTile * D * (fmt == LOOPVQ_MX_E4M3 ? 8 : 4) / 8 + (size_t)kMxTile * (D / kMxBlock);
+}
+
+struct MxLayout {
+  int batch, page_tokens, max_pages, max_ctx, max_new, total_new;
+  int64_t n_pages;      // whole pages of the pool
+  int64_t pool_tiles;   // tiles of one (step, head)
+  const int32_t *pages, *ctx_len, *new_off;
+};
+
+struct MxReq {
+  int ctx, n, base, row0;  // context, new tokens, first new position, first packed row
+};
+// Request r's lengths; false (and the fault bit) if they are out of bounds.
+__device__ __forceinline__ bool mx_request(const MxLayout& L, int r, MxReq* q, uint32_t* fault) {
+  const int ctx = __ldg(L.ctx_len + r), a = __ldg(L.new_off + r), b = __ldg(L.new_off + r + 1);
+  const bool ok = a >= 0 && b >= a && b <= L.total_new && b - a <= L.max_new && ctx >= b - a && ctx <= L.max_ctx;
+  if (!ok) {
+    set_fault(fault, LOOPVQ_FAULT_CTX_RANGE);
+    return false;
+  }
+  q->ctx = ctx;
+  q->n = b - a;
+  q->base = ctx - q->n;
+  q->row0 = a;
+  return true;
+}
+// Pool tile of tile t (tokens 32t ..) of request r, or -1 (and the fault
+// bit) for a page id outside the pool.  The caller has 32t < ctx_len.
+__device__ __forceinline__ int64_t mx_pool_tile(const MxLayout& L, int r, int t, uint32_t* fault) {
+  const int per = L.page_tokens / kMxTile;
+  const int id = __ldg(L.pages + (int64_t)r * L.max_pages + t / per);
+  if (id < 0 || id >= L.n_pages) {
+    set_fault(fault, LOOPVQ_FAULT_POOL_RANGE);
+    return -1;
+  }
+  return (int64_t)id * per + t % per;
+}
+
+// Host checks shared by the entry points.
+loopvq_status mx_check_desc(const loopvq_mx_desc* d);
+loopvq_status mx_check_layout(const loopvq_mx_layout* l, MxLayout* out);
+
+}  // namespace loopvq

@@ -1,0 +1,826 @@
+// Attention of single tokens and of trees of drafted tokens over the
+// microscaled KV cache.
+//
+// Rows: the query rows of a request that read one KV head, row = node * G +
+// query head in the group; a chunk is 8 * NT of them.  A unit is (request, KV
+// head, chunk); the tiles of all units form one list, and every warp of the
+// grid takes the same number of consecutive tiles of it, whatever unit they
+// belong to: ragged batches and single long contexts fill the machine alike.
+// A warp works alone: its ring of tiles is filled by TMA bulk copies that its
+// own lane 0 issues, its softmax state and sums stay in its registers, and a
+// unit that it holds whole is finished there.  A unit that spans warps leaves
+// one partial result per warp, which mx_merge_kernel adds up.
+//
+// Scores: A = 16 query rows x 16 channels, B = the codes of 8 tokens as fp16
+// (exact), fp32 sums per block of 32 channels, times the block's scale in
+// fp32.  The C fragment then holds, in lane (g, c), row g and tokens 4c..4c+3,
+// which is the B operand of the second product: O^T += V^T (16 channels x 16
+// tokens, codes as fp16) x P^T.  No exchange between lanes is needed.
+//
+// A value's scale goes onto the weight: w = 2^(x + e - M), x the score in
+// log2 units, e the scale's exponent, M a reference per row and block of
+// channels, so that the largest weights of each block use fp16's upper range
+// whatever the scales are.  M and the row's own reference m are raised only
+// when a score exceeds m by 10 or a weight exceeds 2^15, which after the first
+// tiles is rare; the sums are rescaled then, and the largest weight stands at
+// 2^8: halfway between fp16's top and where its 11 bits begin to run out, at
+// 2^-22 of the largest weight.
+#include <limits.h>
+
+#include "mx.cuh"
+
+namespace loopvq {
+namespace {
+
+constexpr int kAttnWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kScoreSlack = 10.f, kWeightMax = 32768.f, kWeightExp = 8.f;
+
+template <int D, int FMT>
+struct MxRing {
+  static constexpr int kStages = 3;
+  static constexpr int kSlot = 2 * MxTile<D, FMT>::kBytes;   // K tile, V tile
+  static constexpr int kBytes = kAttnWarps * kStages * kSlot;
+  static constexpr int kCtas = 200 * 1024 / kBytes < 4 ? 200 * 1024 / kBytes : 4;   // per SM
+};
+
+struct MxAttnParams {
+  MxLayout L;
+  int H, Hq, G;
+  const uint8_t *pk, *pv;   // this loop step's pools
+  const void* q;
+  int q_bf16, q_vec;
+  int64_t qn, qh;
+  const uint64_t* tree_mask;
+  float scale, softcap;
+  const float* slopes;
+  void* out;
+  int out_bf16;
+  float* lse;
+  int4* headers;     // per warp: the unit that starts in it and goes on
+  float* partials;   // per warp: 2 slots (a unit that began earlier; one that goes on) of [8 NT][D + 4]
+  int min_tiles;     // least tiles of a warp
+  uint32_t* fault;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
+                                        const uint32_t a3, const uint32_t b0, const uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t h) { return __half22float2(*reinterpret_cast<__half2*>(&h)); }
+// The 4 codes (e4m3) or 8 (e2m1) of a word as fp16 pairs.
+__device__ __forceinline__ void codes_e4m3(uint32_t w, uint32_t* h) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+      : "=r"(h[0]), "=r"(h[1])
+      : "r"(w));
+}
+__device__ __forceinline__ void codes_e2m1(uint32_t w, uint32_t* h) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Scale byte t of a word as 2^e (255: infinity, which codes of 0 turn into NaN).
+__device__ __forceinline__ float scale_f32(uint32_t w, int t) {
+  return __uint_as_float(t == 3 ? (w >> 1) & 0x7f800000u : (w << (23 - 8 * t)) & 0x7f800000u);
+}
+// e4m3 NaN codes to 0.
+__device__ __forceinline__ uint32_t drop_nan_codes(uint32_t w) {
+  const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  return w & ~((m >> 7) * 0xffu);
+}
+
+// Where in the list of tiles a warp is.
+struct MxCursor {
+  int r, u, units, t, tiles;   // request, unit of its H * chunks, tile of its ctx
+};
+// Units and tiles of request r (0 units if it has no part in the call).
+template <int NT>
+__device__ __forceinline__ int mx_units(const MxAttnParams& p, int r, int* tiles) {
+  MxReq q;
+  *tiles = 0;
+  if (!mx_request(p.L, r, &q, p.fault) || q.n == 0 || q.n > kMxMaxTree) return 0;
+  *tiles = (q.ctx + kMxTile - 1) / kMxTile;
+  return (q.n * p.G + 8 * NT - 1) / (8 * NT) * p.H;
+}
+// The cursor at tile `at` of the whole list (0 <= at < total); uniform in the warp.
+template <int NT>
+__device__ __forceinline__ MxCursor mx_seek(const MxAttnParams& p, int64_t at, int lane) {
+  MxCursor c = {0, 0, 0, 0, 1};
+  for (int r0 = 0; r0 < p.L.batch; r0 += 32) {
+    int tiles = 0, units = 0;
+    if (r0 + lane < p.L.batch) units = mx_units<NT>(p, r0 + lane, &tiles);
+    int64_t sum = (int64_t)units * tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += o;
+    }
+    const int64_t all = __shfl_sync(0xffffffffu, sum, 31);
+    if (at < all) {
+      const int l = __ffs(__ballot_sync(0xffffffffu, at < sum)) - 1;
+      c.r = r0 + l;
+      c.units = __shfl_sync(0xffffffffu, units, l);
+      c.tiles = __shfl_sync(0xffffffffu, tiles, l);
+      const int64_t in = at - (__shfl_sync(0xffffffffu, sum, l) - (int64_t)c.units * c.tiles);
+      c.u = (int)(in / c.tiles);
+      c.t = (int)(in % c.tiles);
+      return c;
+    }
+    at -= all;
+  }
+  return c;
+}
+// On to the next unit; the caller knows that there is one (lengths that
+// change under the kernel are the caller's error; indices stay in range).
+template <int NT>
+__device__ __forceinline__ void mx_next_unit(const MxAttnParams& p, MxCursor* c) {
+  c->t = 0;
+  if (++c->u < c->units) return;
+  c->u = 0;
+  do {
+    if (++c->r >= p.L.batch) {
+      c->r = p.L.batch - 1;
+      c->units = p.H;
+      c->tiles = 1;
+      return;
+    }
+    c->units = mx_units<NT>(p, c->r, &c->tiles);
+  } while (c->units == 0);
+}
+
+template <int D, int FMT, int TERMS, int NT>
+__global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_attn_kernel(const MxAttnParams p) {
+  using Tile = MxTile<D, FMT>;
+  using Ring = MxRing<D, FMT>;
+  constexpr int NB = Tile::kBlocks, S = Ring::kStages;
+  constexpr int MT = TERMS == 2 ? NT : (NT + 1) / 2;   // 16-row operands of the score product
+  constexpr int kHalves = TERMS == 1 && NT == 1 ? 1 : 2;
+  extern __shared__ __align__(128) uint8_t sm_ring[];
+  __shared__ __align__(8) uint64_t bars[kAttnWarps][S];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  const int n_warps = gridDim.x * kAttnWarps, wid = blockIdx.x * kAttnWarps + warp;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  // this warp's share of the list
+  int64_t total = 0;
+  for (int r = lane; r < p.L.batch; r += 32) {
+    int tiles;
+    const int units = mx_units<NT>(p, r, &tiles);
+    total += (int64_t)units * tiles;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+  int64_t share = (total + n_warps - 1) / n_warps;
+  if (share < p.min_tiles) share = p.min_tiles;
+  const int64_t begin = wid * share;
+  const int64_t left = total - begin;
+  const int count = left <= 0 ? 0 : (int)(left < share ? left : share);
+  if (lane == 0) p.headers[wid] = make_int4(0, 0, 0, 0);
+  if (count == 0) return;
+
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  uint8_t* ring = sm_ring + warp * S * Ring::kSlot;
+
+  MxCursor cc = mx_seek<NT>(p, begin, lane);   // consumer
+  MxCursor pc = cc;                            // producer
+  const int per = p.L.page_tokens / kMxTile;
+  int page = pc.t / per, in_page = pc.t % per, issued = 0;
+  uint32_t bad = 0;   // bit per slot: its tile's page is not in the pool
+  auto page_id = [&]() { return __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page); };
+  int id = page_id();
+  auto issue = [&](int slot) {
+    const bool ok = id >= 0 && id < p.L.n_pages;
+    bad = (bad & ~(1u << slot)) | (ok ? 0u : 1u << slot);
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(&bars[warp][slot]);
+      if (ok) {
+        const int chunks = pc.units / p.H;
+        const int64_t at = ((int64_t)(pc.u / chunks) * p.L.pool_tiles + (int64_t)id * per + in_page) * Tile::kBytes;
+        const uint32_t dst = smem_u32(ring + slot * Ring::kSlot);
+        mbar_arrive_expect_tx(bar, 2 * Tile::kBytes);
+        bulk_g2s(dst, p.pk + at, Tile::kBytes, bar);
+        bulk_g2s(dst + Tile::kBytes, p.pv + at, Tile::kBytes, bar);
+      } else {
+        set_fault(p.fault, LOOPVQ_FAULT_POOL_RANGE);
+        mbar_arrive(bar);
+      }
+    }
+    if (++issued < count) {
+      if (++pc.t == pc.tiles) {
+        mx_next_unit<NT>(p, &pc);
+        page = in_page = 0;
+        id = page_id();
+      } else if (++in_page == per) {
+        in_page = 0;
+        ++page;
+        id = page_id();
+      }
+    }
+  };
+  for (int i = 0; i < S && i < count; ++i) issue(i);
+
+  int done = 0, slot = 0;
+  uint32_t phase = 0;
+  bool lost = false;
+  while (done < count && !lost) {
+    // ------------------------------------------------ a unit, or the part of it in this share
+    MxReq rq = {};
+    mx_request(p.L, cc.r, &rq, nullptr);
+    const int chunks = cc.units / p.H, h = cc.u / chunks, rho0 = (cc.u - h * chunks) * (8 * NT);
+    const int rows = min(8 * NT, rq.n * p.G - rho0);
+    const int first_tile = cc.t, n_tiles = min(cc.tiles - cc.t, count - done);
+    const uint64_t all_new = rq.n >= 64 ? ~0ull : (1ull << rq.n) - 1;
+
+    // query rows: scaled by a power of two to a largest magnitude in [2^14, 2^15), as fp16 (TERMS = 2: and the rest)
+    uint32_t qa[MT][NB][2][4] = {};
+    float f[NT], slope[NT];
+    uint64_t sees[NT];
+    int pos_q[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const int rho = rho0 + 8 * i + g;
+      f[i] = slope[i] = 0.f;
+      sees[i] = 0;
+      pos_q[i] = 0;
+      float v[NB][8];
+      float mx = 0.f;
+      const bool there = rho < rq.n * p.G;
+      if (there) {
+        const int node = rho / p.G, hq = h * p.G + rho % p.G;
+        const int64_t at = (int64_t)(rq.row0 + node) * p.qn + (int64_t)hq * p.qh + 8 * c;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          if (p.q_bf16) {
+            const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(p.q) + at + 32 * b;
+            if (p.q_vec) {
+              const uint4 w = __ldg(reinterpret_cast<const uint4*>(x));
+              v[b][0] = bf16_lo(w.x); v[b][1] = bf16_hi(w.x); v[b][2] = bf16_lo(w.y); v[b][3] = bf16_hi(w.y);
+              v[b][4] = bf16_lo(w.z); v[b][5] = bf16_hi(w.z); v[b][6] = bf16_lo(w.w); v[b][7] = bf16_hi(w.w);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) v[b][k] = __bfloat162float(x[k]);
+            }
+          } else {
+            const float* x = reinterpret_cast<const float*>(p.q) + at + 32 * b;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[b][k] = __ldg(x + k);
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(v[b][k]));
+        }
+        sees[i] = (p.tree_mask ? __ldg(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
+        pos_q[i] = rq.base + __popcll(sees[i] & ~(1ull << node));
+        if (p.slopes) slope[i] = __ldg(p.slopes + hq) * kLog2e;
+      } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[b][k] = 0.f;
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // 2^k: mx = frac * 2^ex, ex the exponent field's value (subnormals count as the least)
+      const int ex = max((int)(__float_as_uint(mx) >> 23), 1) - 127;
+      const int k2 = min(14 - ex, 120);
+      const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
+      f[i] = p.softcap > 0.f ? p.scale / p.softcap * down : p.scale * kLog2e * down;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x0 = v[b][2 * k] * up, x1 = v[b][2 * k + 1] * up;
+          const uint32_t hi = pack_f16(x0, x1);
+          // pair k: channels 8c + 2k, 8c + 2k + 1: product k/2, upper half of its 16 channels if k is odd
+          if constexpr (TERMS == 1) {
+            qa[i / 2][b][k >> 1][(k & 1) * 2 + (i & 1)] = hi;
+          } else {
+            const float2 b2 = unpack_f16(hi);
+            qa[i][b][k >> 1][(k & 1) * 2] = hi;
+            qa[i][b][k >> 1][(k & 1) * 2 + 1] = pack_f16(x0 - b2.x, x1 - b2.y);
+          }
+        }
+    }
+
+    float m[NT], l[NT], M[NT][NB], rs[NT][NB], o[NB][2][NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        M[i][b] = -INFINITY;
+        rs[i][b] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[b][0][i][k] = o[b][1][i][k] = 0.f;
+      }
+    }
+
+    for (int it = 0; it < n_tiles; ++it) {
+      const bool got = mbar_wait_bounded(smem_u32(&bars[warp][slot]), phase);
+      if (!__all_sync(0xffffffffu, got)) {
+        if (lane == 0) set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
+        lost = true;
+        break;
+      }
+      const uint8_t* sk = ring + slot * Ring::kSlot;
+      const uint8_t* sv = sk + Tile::kBytes;
+      const int tok0 = (first_tile + it) * kMxTile;
+      const bool edge = tok0 + kMxTile > rq.base;
+      if (!(bad >> slot & 1)) {
+#pragma unroll 1
+        for (int sub = 0; sub < 2; ++sub) {
+          // ---- scores
+          float s[MT][2][4] = {};
+          uint32_t scw[NB];
+          {
+            const uint8_t* z = sk + mx_scale_off<D, FMT>(sub * 4 + c, 0);
+            if constexpr (NB == 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(z);
+              scw[0] = w.x; scw[1] = w.y; scw[2] = w.z; scw[3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(z);
+              scw[0] = w.x; scw[1] = w.y;
+            }
+          }
+#pragma unroll
+          for (int b = 0; b < NB; b += 2) {
+            uint32_t h[2][2][4];   // [block][ab][pair]
+            if constexpr (FMT == LOOPVQ_MX_E4M3) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint4 w = *reinterpret_cast<const uint4*>(sk + mx_code_off<D, FMT>(sub, b + k, lane));
+                codes_e4m3(w.x, h[k][0]);
+                codes_e4m3(w.y, h[k][0] + 2);
+                codes_e4m3(w.z, h[k][1]);
+                codes_e4m3(w.w, h[k][1] + 2);
+              }
+            } else {
+              const uint4 w = *reinterpret_cast<const uint4*>(sk + mx_code_off<D, FMT>(sub, b, lane));
+              codes_e2m1(w.x, h[0][0]);
+              codes_e2m1(w.y, h[0][1]);
+              codes_e2m1(w.z, h[1][0]);
+              codes_e2m1(w.w, h[1][1]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int ab = 0; ab < 2; ++ab) {
+                const float s0 = scale_f32(scw[b + k], 2 * ab), s1 = scale_f32(scw[b + k], 2 * ab + 1);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                  float d[4] = {0.f, 0.f, 0.f, 0.f};
+                  const uint32_t(*a)[4] = qa[i][b + k];
+                  mma_f16(d, a[0][0], a[0][1], a[0][2], a[0][3], h[k][ab][0], h[k][ab][1]);
+                  mma_f16(d, a[1][0], a[1][1], a[1][2], a[1][3], h[k][ab][2], h[k][ab][3]);
+                  s[i][ab][0] = fmaf(d[0], s0, s[i][ab][0]);
+                  s[i][ab][1] = fmaf(d[1], s1, s[i][ab][1]);
+                  if constexpr (kHalves == 2) {
+                    s[i][ab][2] = fmaf(d[2], s0, s[i][ab][2]);
+                    s[i][ab][3] = fmaf(d[3], s1, s[i][ab][3]);
+                  }
+                }
+              }
+          }
+          // ---- in log2 units, with cap, bias and mask: row g of group i, tokens 4c + t
+          const int pos = tok0 + 16 * sub + 4 * c;
+          float x[NT][4];
+          uint32_t hide = 0;   // bit 4i + t: not seen
+#pragma unroll
+          for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              float y = TERMS == 2 ? s[i % MT][t >> 1][t & 1] + s[i % MT][t >> 1][2 + (t & 1)]
+                                   : s[i / 2][t >> 1][2 * (i & 1) + (t & 1)];
+              y *= f[i];
+              if (p.softcap > 0.f) y = p.softcap * kLog2e * tanhf(y);
+              x[i][t] = y;
+            }
+          if (p.slopes || edge) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const int j = pos + t - rq.base;   // >= 0: a new token
+              int at = pos + t;
+              if (p.slopes && j >= 0 && j < rq.n) {
+                const uint64_t its = p.tree_mask ? __ldg(p.tree_mask + rq.row0 + j) & all_new : (2ull << j) - 1;
+                at = rq.base + __popcll(its & ~(1ull << j));
+              }
+#pragma unroll
+              for (int i = 0; i < NT; ++i) {
+                if (p.slopes) x[i][t] -= slope[i] * (float)(pos_q[i] - at);
+                const bool see = j < 0 || (j < rq.n && (sees[i] >> j & 1));
+                if (!see) {
+                  x[i][t] = -INFINITY;
+                  hide |= 1u << (4 * i + t);
+                }
+              }
+            }
+          }
+          // ---- weights
+          uint32_t vcw[NB];
+          {
+            const uint8_t* z = sv + mx_scale_off<D, FMT>(sub * 4 + c, 0);
+            if constexpr (NB == 4) {
+              const uint4 w = *reinterpret_cast<const uint4*>(z);
+              vcw[0] = w.x; vcw[1] = w.y; vcw[2] = w.z; vcw[3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(z);
+              vcw[0] = w.x; vcw[1] = w.y;
+            }
+          }
+          uint32_t pw[NT][NB][TERMS][2];
+          float pr[NT];
+          auto weights = [&]() {
+            bool over = false;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              const float mi = m[i] == -INFINITY ? 0.f : m[i];
+              float e[4];
+#pragma unroll
+              for (int t = 0; t < 4; ++t) e[t] = ex2(x[i][t] - mi);
+              pr[i] = (e[0] + e[1]) + (e[2] + e[3]);
+              over |= fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])) > m[i] + kScoreSlack;
+              float wm = 0.f;
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                float w[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t) w[t] = e[t] * scale_f32(vcw[b], t) * rs[i][b];
+                if (edge) {
+#pragma unroll
+                  for (int t = 0; t < 4; ++t)
+                    if (hide >> (4 * i + t) & 1) w[t] = 0.f;
+                }
+                wm = fmaxf(wm, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  pw[i][b][0][k] = pack_f16(w[2 * k], w[2 * k + 1]);
+                  if constexpr (TERMS == 2) {
+                    const float2 hi = unpack_f16(pw[i][b][0][k]);
+                    pw[i][b][1][k] = pack_f16(w[2 * k] - hi.x, w[2 * k + 1] - hi.y);
+                  }
+                }
+              }
+              over |= wm > kWeightMax;
+            }
+            return over;
+          };
+          if (__any_sync(0xffffffffu, weights())) {
+            // raise the references to what has been seen, and bring the sums to them
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+              float mx = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3]));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+              const float mn = fmaxf(m[i], mx);
+              if (m[i] != -INFINITY) l[i] *= ex2(m[i] - mn);
+              m[i] = mn;
+#pragma unroll
+              for (int b = 0; b < NB; ++b) {
+                float bm = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < 4; ++t) bm = fmaxf(bm, x[i][t] + (float)((int)(vcw[b] >> (8 * t) & 255u) - 127));
+                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+                const float Mn = fmaxf(M[i][b], bm - kWeightExp);
+                const float fb = M[i][b] == -INFINITY ? 0.f : ex2(M[i][b] - Mn);
+                M[i][b] = Mn;
+                rs[i][b] = Mn == -INFINITY ? 0.f : ex2(mn - Mn);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const float fc = __shfl_sync(0xffffffffu, fb, (2 * c + k) * 4);
+#pragma unroll
+                  for (int a = 0; a < 2; ++a) {
+                    o[b][a][i][k] *= fc;
+                    o[b][a][i][2 + k] *= fc;
+                  }
+                }
+              }
+            }
+            weights();
+          }
+#pragma unroll
+          for (int i = 0; i < NT; ++i) l[i] += pr[i];
+          // ---- values
+#pragma unroll
+          for (int b = 0; b < NB; b += 2) {
+            uint32_t h[2][4][2];   // [block][channel j][token pair]
+            if constexpr (FMT == LOOPVQ_MX_E4M3) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint4 w = *reinterpret_cast<const uint4*>(sv + mx_code_off<D, FMT>(sub, b + k, lane));
+                if (edge) {
+                  w.x = drop_nan_codes(w.x);
+                  w.y = drop_nan_codes(w.y);
+                  w.z = drop_nan_codes(w.z);
+                  w.w = drop_nan_codes(w.w);
+                }
+                codes_e4m3(w.x, h[k][0]);
+                codes_e4m3(w.y, h[k][1]);
+                codes_e4m3(w.z, h[k][2]);
+                codes_e4m3(w.w, h[k][3]);
+              }
+            } else {
+              const uint4 w = *reinterpret_cast<const uint4*>(sv + mx_code_off<D, FMT>(sub, b, lane));
+              codes_e2m1(w.x, h[0][0]);
+              codes_e2m1(w.y, h[0][2]);
+              codes_e2m1(w.z, h[1][0]);
+              codes_e2m1(w.w, h[1][2]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                  for (int e = 0; e < TERMS; ++e)
+                    mma_f16(o[b + k][a][i], h[k][2 * a][0], h[k][2 * a + 1][0], h[k][2 * a][1], h[k][2 * a + 1][1],
+                            pw[i][b + k][e][0], pw[i][b + k][e][1]);
+          }
+        }
+      }
+      __syncwarp();   // every lane has read the slot
+      if (issued < count) issue(slot);
+      ++done;
+      if (++slot == S) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+    if (lost) break;
+
+    // ------------------------------------------------ the unit's rows, or this warp's part of them
+    const bool whole = first_tile == 0 && n_tiles == cc.tiles;
+    float* part = p.partials + (size_t)(2 * wid + (first_tile == 0)) * (8 * NT) * (D + 4);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      float ls = l[i];
+      ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+      ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+      const int mine = 8 * i + g;
+      const float lse = ls == 0.f ? -INFINITY : (m[i] + log2f(ls)) * kLn2;
+      if (c == 0 && mine < rows) {
+        const int rho = rho0 + mine;
+        if (!whole) {
+          part[mine * (D + 4) + D] = m[i];
+          part[mine * (D + 4) + D + 1] = ls;
+        } else if (p.lse) {
+          p.lse[(int64_t)(rq.row0 + rho / p.G) * p.Hq + h * p.G + rho % p.G] = lse;
+        }
+      }
+      const float inv = whole ? (ls == 0.f ? 0.f : 1.f / ls) : 1.f;
+      float fb[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) fb[b] = M[i][b] == -INFINITY ? (ls == 0.f ? 0.f : ls) : ex2(M[i][b] - m[i]) * inv;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = 8 * i + 2 * c + k, rho = rho0 + row;
+        const int64_t at = ((int64_t)(rq.row0 + rho / p.G) * p.Hq + h * p.G + rho % p.G) * D;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float fc = __shfl_sync(0xffffffffu, fb[b], (2 * c + k) * 4);
+          if (row >= rows) continue;
+          const float4 y = make_float4(o[b][0][i][k] * fc, o[b][0][i][2 + k] * fc, o[b][1][i][k] * fc,
+                                       o[b][1][i][2 + k] * fc);
+          if (!whole) {
+            *reinterpret_cast<float4*>(part + row * (D + 4) + 32 * b + 4 * g) = y;
+          } else if (p.out_bf16) {
+            const __nv_bfloat162 u0 = __floats2bfloat162_rn(y.x, y.y), u1 = __floats2bfloat162_rn(y.z, y.w);
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at + 32 * b + 4 * g) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&u0), *reinterpret_cast<const uint32_t*>(&u1));
+          } else {
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at + 32 * b + 4 * g) = y;
+          }
+        }
+      }
+    }
+    if (first_tile == 0 && !whole && lane == 0) {
+      // the warps after this one that hold the unit's other tiles
+      const int rest = cc.tiles - n_tiles;
+      p.headers[wid] = make_int4((int)((rest + share - 1) / share), rq.row0, h, rho0 << 8 | rows);
+    }
+    if (done < count) mx_next_unit<NT>(p, &cc);
+  }
+  if (lost) {   // copies that are still on their way end before the block does
+    for (int i = done; i < issued; ++i) {
+      mbar_wait_bounded(smem_u32(&bars[warp][slot]), phase);
+      if (++slot == S) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+  }
+}
+
+// Adds up a unit's partial results.  Block (w, y) takes the unit that starts
+// in warp w and goes on in warps after it, rows y, y + gridDim.y, ..; each of
+// its warps sums every fourth part relative to the row's largest reference.
+constexpr int kMergeWarps = 4;
+template <int D, int NT>
+__global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttnParams p) {
+  constexpr int kCh = D / 32;   // channels of a lane
+  __shared__ float sm_o[kMergeWarps][D];
+  __shared__ float sm_l[kMergeWarps];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 hd = __ldcg(p.headers + w);
+  if (hd.x == 0) return;
+  const int rows = hd.w & 255, rho0 = hd.w >> 8;
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+    auto part = [&](int k) {   // slot 1 of warp w, slot 0 of the next ones
+      return p.partials + ((size_t)(2 * (w + k) + (k == 0)) * (8 * NT) + row) * (D + 4);
+    };
+    float mx = -INFINITY;
+    for (int k = lane; k <= hd.x; k += 32) mx = fmaxf(mx, __ldcg(part(k) + D));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    const float m0 = mx == -INFINITY ? 0.f : mx;
+    float l = 0.f, o[kCh] = {};
+#pragma unroll 4
+    for (int k = warp; k <= hd.x; k += kMergeWarps) {
+      const float* q = part(k);
+      const float f = ex2(__ldcg(q + D) - m0);
+      l += __ldcg(q + D + 1) * f;
+      if constexpr (kCh == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + lane);
+        o[0] = fmaf(v.x, f, o[0]);
+        o[1] = fmaf(v.y, f, o[1]);
+        o[2] = fmaf(v.z, f, o[2]);
+        o[3] = fmaf(v.w, f, o[3]);
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(q) + lane);
+        o[0] = fmaf(v.x, f, o[0]);
+        o[1] = fmaf(v.y, f, o[1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCh; ++i) sm_o[warp][lane * kCh + i] = o[i];
+    if (lane == 0) sm_l[warp] = l;
+    __syncthreads();
+    float ls = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMergeWarps; ++i) ls += sm_l[i];
+    const int rho = rho0 + row;
+    const int64_t at = (int64_t)(hd.y + rho / p.G) * p.Hq + hd.z * p.G + rho % p.G;
+    const float inv = ls == 0.f ? 0.f : 1.f / ls;
+    const int d = threadIdx.x;
+    if (d < D) {
+      float y = 0.f;
+#pragma unroll
+      for (int i = 0; i < kMergeWarps; ++i) y += sm_o[i][d];
+      y *= inv;
+      if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + d] = __float2bfloat16_rn(y);
+      else reinterpret_cast<float*>(p.out)[at * D + d] = y;
+    }
+    if (d == 0 && p.lse) p.lse[at] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * kLn2;
+    __syncthreads();
+  }
+}
+
+// Rows of a chunk: 16 where a request can have more than 8 (the codes are
+// converted once for both halves), else 8.
+int attn_groups(const loopvq_mx_desc* d, const loopvq_mx_layout* l) {
+  return (int64_t)l->max_new * (d->n_heads_q / d->n_heads_kv) > 8 ? 2 : 1;
+}
+int attn_ctas(int D, int fmt) {
+  const int n = device_sm_count();
+  if (D == 128) return n * (fmt == LOOPVQ_MX_E4M3 ? MxRing<128, LOOPVQ_MX_E4M3>::kCtas : MxRing<128, LOOPVQ_MX_E2M1>::kCtas);
+  return n * (fmt == LOOPVQ_MX_E4M3 ? MxRing<64, LOOPVQ_MX_E4M3>::kCtas : MxRing<64, LOOPVQ_MX_E2M1>::kCtas);
+}
+constexpr int kMinTiles = 2;
+// Blocks of the launch: no more than the warps that could get their least share.
+int attn_grid(const loopvq_mx_desc* d, const loopvq_mx_layout* l) {
+  const int nt = attn_groups(d, l);
+  const int64_t rows = (int64_t)l->max_new * (d->n_heads_q / d->n_heads_kv);
+  const int64_t chunks = (rows + 8 * nt - 1) / (8 * nt), tiles = ((int64_t)l->max_ctx_len + kMxTile - 1) / kMxTile;
+  const int most = attn_ctas(d->head_dim, d->format);
+  const int64_t each = (int64_t)d->n_heads_kv * chunks;   // all products below stay under 2^63: see the checks
+  const int64_t per_cta = (int64_t)kMinTiles * kAttnWarps;
+  if (each * tiles >= most * per_cta) return most;
+  const int64_t n = (each * tiles * l->batch + per_cta - 1) / per_cta;
+  return n < 1 ? 1 : n < most ? (int)n : most;
+}
+
+template <int D, int FMT, int TERMS, int NT>
+loopvq_status launch_attn(const MxAttnParams& p, int grid, int rows, cudaStream_t s) {
+  constexpr int smem = MxRing<D, FMT>::kBytes;
+  auto kfn = mx_attn_kernel<D, FMT, TERMS, NT>;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  kfn<<<grid, kAttnWarps * 32, smem, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid * kAttnWarps, rows < 8 * NT ? rows : 8 * NT);
+  cfg.blockDim = dim3(kMergeWarps * 32);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, NT>, p) == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+}
+
+loopvq_status attn_checks(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout, MxLayout* L) {
+  loopvq_status st = mx_check_desc(desc);
+  if (st != LOOPVQ_OK) return st;
+  st = mx_check_layout(layout, L);
+  if (st != LOOPVQ_OK) return st;
+  return layout->max_new > kMxMaxTree ? LOOPVQ_ERR_UNSUPPORTED : LOOPVQ_OK;
+}
+struct AttnWs {
+  size_t partials_off, total;
+};
+AttnWs attn_ws(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout) {
+  const size_t warps = (size_t)attn_grid(desc, layout) * kAttnWarps;
+  AttnWs w;
+  w.partials_off = (warps * sizeof(int4) + 255) & ~(size_t)255;
+  w.total = w.partials_off + warps * 2 * 8 * attn_groups(desc, layout) * (desc->head_dim + 4) * sizeof(float);
+  return w;
+}
+
+}  // namespace
+}  // namespace loopvq
+
+using namespace loopvq;
+
+extern "C" size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout) {
+  MxLayout L;
+  if (attn_checks(desc, layout, &L) != LOOPVQ_OK) return 0;
+  return attn_ws(desc, layout).total;
+}
+
+extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
+                                        const void* poolK, const void* poolV, const void* q, loopvq_dtype q_dtype,
+                                        int64_t q_stride_n, int64_t q_stride_h, const uint64_t* tree_mask,
+                                        int32_t loop_step, float softmax_scale, float softcap, const float* slopes,
+                                        void* out, loopvq_dtype out_dtype, float* lse_out, void* workspace,
+                                        size_t workspace_bytes, uint32_t* fault_bits, loopvq_stream_t stream) {
+  MxAttnParams p = {};
+  const loopvq_status st = attn_checks(desc, layout, &p.L);
+  if (st != LOOPVQ_OK) return st;
+  if (loop_step < 0 || loop_step >= desc->n_loop) return LOOPVQ_ERR_INVALID_ARG;
+  if (!poolK || !poolV || ((uintptr_t)poolK & 15) || ((uintptr_t)poolV & 15)) return LOOPVQ_ERR_INVALID_ARG;
+  if ((q_dtype != LOOPVQ_F32 && q_dtype != LOOPVQ_BF16) || (out_dtype != LOOPVQ_F32 && out_dtype != LOOPVQ_BF16))
+    return LOOPVQ_ERR_INVALID_ARG;
+  if (q_stride_n < 0 || q_stride_h < 0 || !(softcap >= 0.f) || !(softcap <= 3.0e38f) ||
+      !(softmax_scale >= -3.0e38f && softmax_scale <= 3.0e38f))
+    return LOOPVQ_ERR_INVALID_ARG;
+  if (((uintptr_t)tree_mask & 7) || ((uintptr_t)slopes & 3) || ((uintptr_t)lse_out & 3) || ((uintptr_t)fault_bits & 3))
+    return LOOPVQ_ERR_INVALID_ARG;
+  if (layout->total_new == 0 || layout->max_new == 0 || layout->max_ctx_len == 0) return LOOPVQ_OK;
+  const uintptr_t qs = q_dtype == LOOPVQ_BF16 ? 2 : 4;
+  if (!q || (uintptr_t)q % qs || !out || ((uintptr_t)out & 15)) return LOOPVQ_ERR_INVALID_ARG;
+  if (!workspace || ((uintptr_t)workspace & 255)) return LOOPVQ_ERR_INVALID_ARG;
+  const AttnWs ws = attn_ws(desc, layout);
+  if (workspace_bytes < ws.total) return LOOPVQ_ERR_WORKSPACE_TOO_SMALL;
+  const size_t step = (size_t)desc->n_heads_kv * p.L.pool_tiles * mx_tile_bytes(desc->head_dim, desc->format);
+  p.H = desc->n_heads_kv;
+  p.Hq = desc->n_heads_q;
+  p.G = p.Hq / p.H;
+  p.pk = (const uint8_t*)poolK + loop_step * step;
+  p.pv = (const uint8_t*)poolV + loop_step * step;
+  p.q = q;
+  p.q_bf16 = q_dtype == LOOPVQ_BF16;
+  p.q_vec = !(((uintptr_t)q | (uintptr_t)q_stride_n * qs | (uintptr_t)q_stride_h * qs) & 15);
+  p.qn = q_stride_n;
+  p.qh = q_stride_h;
+  p.tree_mask = tree_mask;
+  p.scale = softmax_scale;
+  p.softcap = softcap;
+  p.slopes = slopes;
+  p.out = out;
+  p.out_bf16 = out_dtype == LOOPVQ_BF16;
+  p.lse = lse_out;
+  p.headers = (int4*)workspace;
+  p.partials = (float*)((uint8_t*)workspace + ws.partials_off);
+  p.min_tiles = kMinTiles;
+  p.fault = fault_bits;
+  const int grid = attn_grid(desc, layout), nt = attn_groups(desc, layout);
+  const int rows = (int)((int64_t)layout->max_new * p.G < 16 ? layout->max_new * p.G : 16);
+  const bool fine = q_dtype == LOOPVQ_F32 || out_dtype == LOOPVQ_F32;   // two fp16 terms of q and of the weights
+  cudaStream_t s = (cudaStream_t)stream;
+#define MX_ATTN_NT(D_, F_)                                                                                        \
+  (fine ? (nt == 2 ? launch_attn<D_, F_, 2, 2>(p, grid, rows, s) : launch_attn<D_, F_, 2, 1>(p, grid, rows, s))   \
+        : (nt == 2 ? launch_attn<D_, F_, 1, 2>(p, grid, rows, s) : launch_attn<D_, F_, 1, 1>(p, grid, rows, s)))
+  if (desc->head_dim == 128)
+    return desc->format == LOOPVQ_MX_E4M3 ? MX_ATTN_NT(128, LOOPVQ_MX_E4M3) : MX_ATTN_NT(128, LOOPVQ_MX_E2M1);
+  return desc->format == LOOPVQ_MX_E4M3 ? MX_ATTN_NT(64, LOOPVQ_MX_E4M3) : MX_ATTN_NT(64, LOOPVQ_MX_E2M1);
+}

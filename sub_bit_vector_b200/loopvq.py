@@ -27,6 +27,9 @@ LOOPVQ_BF16 = 1
 LOOPVQ_KEYS = 0
 LOOPVQ_VALUES = 1
 
+LOOPVQ_MX_E4M3 = 0
+LOOPVQ_MX_E2M1 = 1
+
 LOOPVQ_FAULT_CODE_RANGE = 0x1
 LOOPVQ_FAULT_CTX_RANGE = 0x2
 LOOPVQ_FAULT_POOL_RANGE = 0x4
@@ -46,6 +49,8 @@ EXPORTED = [
     "loopvq_decode_steps_workspace_bytes", "loopvq_decode_attn_steps",
     "loopvq_residual_codes_bytes", "loopvq_residual_params_bytes", "loopvq_residual_encode",
     "loopvq_residual_decode_workspace_bytes", "loopvq_residual_decode_attn",
+    "loopvq_mx_pool_bytes", "loopvq_mx_write", "loopvq_mx_read", "loopvq_mx_attn_workspace_bytes",
+    "loopvq_mx_attn", "loopvq_mx_keep",
     "loopvq_read_device_status",
     "loopvq_clear_device_status", "loopvq_dense_decode_workspace_bytes", "loopvq_dense_decode_attn",
 ]
@@ -68,6 +73,18 @@ class loopvq_residual_desc(ctypes.Structure):
                 ("head_dim", ctypes.c_int32)]
 
 
+class loopvq_mx_desc(ctypes.Structure):
+    _fields_ = [("n_loop", ctypes.c_int32), ("n_heads_kv", ctypes.c_int32), ("n_heads_q", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int)]
+
+
+class loopvq_mx_layout(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_ctx_len", ctypes.c_int32), ("max_new", ctypes.c_int32), ("total_new", ctypes.c_int32),
+                ("pool_tokens", ctypes.c_int64), ("pages", ctypes.c_void_p), ("ctx_len", ctypes.c_void_p),
+                ("new_off", ctypes.c_void_p)]
+
+
 class loopvq_cache_layout(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("n_sink", ctypes.c_int32), ("n_recent", ctypes.c_int32),
                 ("page", ctypes.c_int32), ("max_ctx_len", ctypes.c_int32), ("flags", ctypes.c_uint32),
@@ -87,6 +104,7 @@ def _load() -> ctypes.CDLL:
     D = ctypes.POINTER(loopvq_codebook_desc)
     L = ctypes.POINTER(loopvq_cache_layout)
     RD = ctypes.POINTER(loopvq_residual_desc)
+    MD, ML = ctypes.POINTER(loopvq_mx_desc), ctypes.POINTER(loopvq_mx_layout)
     sig = {
         "loopvq_version": (ctypes.c_char_p, []),
         "loopvq_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -113,6 +131,13 @@ def _load() -> ctypes.CDLL:
         "loopvq_residual_decode_workspace_bytes": (SZ, [RD, I32, I32]),
         "loopvq_residual_decode_attn": (ctypes.c_int, [RD, I32, I32, P, P, I64, U8P, P, U8P, P, P, ctypes.c_int, I32,
                                                        F, P, P, P, SZ, P]),
+        "loopvq_mx_pool_bytes": (SZ, [MD, I64]),
+        "loopvq_mx_write": (ctypes.c_int, [MD, ML, I32, I32, P, P, ctypes.c_int, I64, I64, I64, P, P, P, P]),
+        "loopvq_mx_read": (ctypes.c_int, [MD, ML, I32, I32, P, P, P, P, ctypes.c_int, I64, I64, I64, P, P]),
+        "loopvq_mx_attn_workspace_bytes": (SZ, [MD, ML]),
+        "loopvq_mx_attn": (ctypes.c_int, [MD, ML, P, P, P, ctypes.c_int, I64, I64, P, I32, F, F, P, P, ctypes.c_int, P,
+                                          P, SZ, P, P]),
+        "loopvq_mx_keep": (ctypes.c_int, [MD, ML, P, P, I32, P, P, P, P]),
         "loopvq_decode_workspace_bytes": (SZ, [D, L]),
         "loopvq_decode_attn": (ctypes.c_int, [D, P, P, L, U8P, U8P, P, P, P, ctypes.c_int, I32, F, P,
                                               ctypes.c_int, P, P, SZ, P]),
@@ -310,6 +335,176 @@ def loopvq_residual_decode_attn(desc, batch, max_ctx_len, ctx_len, tok_off, pool
         ctypes.byref(desc), batch, max_ctx_len, _ptr(ctx_len), _ptr(tok_off), pool_tokens, _ptr(codesK),
         _ptr(paramsK), _ptr(codesV), _ptr(paramsV), _ptr(q), _dtype_code(q), loop_step, softmax_scale, _ptr(out),
         _ptr(lse_out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+# ------------------------------------------------- microscaled KV cache
+
+def make_mx_desc(n_loop, n_heads_kv, head_dim, format, n_heads_q=None) -> loopvq_mx_desc:
+    return loopvq_mx_desc(n_loop, n_heads_kv, n_heads_q or n_heads_kv, head_dim, format)
+
+
+def make_mx_layout(batch, page_tokens, max_pages, pool_tokens, max_ctx_len, max_new, total_new, ctx_len, new_off,
+                   pages) -> loopvq_mx_layout:
+    for name, t, n in (("ctx_len", ctx_len, batch), ("new_off", new_off, batch + 1), ("pages", pages, batch * max_pages)):
+        _want(name, t, ("int32",), n)
+    lay = loopvq_mx_layout(batch, page_tokens, max_pages, max_ctx_len, max_new, total_new, pool_tokens, _ptr(pages),
+                           _ptr(ctx_len), _ptr(new_off))
+    lay._keep = (ctx_len, new_off, pages)
+    return lay
+
+
+def _want(name, t, dtypes, n) -> None:
+    """The kernels read ``n`` consecutive elements of ``t``: its type, order
+    and length must be right.  Raw addresses (and None) pass unchecked."""
+    if t is None or isinstance(t, int):
+        return
+    if str(t.dtype).split(".")[-1] not in dtypes:
+        raise TypeError(f"{name}: {t.dtype} where {' or '.join(dtypes)} is needed")
+    if not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{name}: {n} consecutive elements are needed")
+
+
+def _want_strided(name, t, last) -> None:
+    """The kernels read or write ``t`` up to element ``last``."""
+    if t is None or isinstance(t, int):
+        return
+    if (t.storage_offset() + last + 1) * t.element_size() > t.untyped_storage().nbytes():
+        raise ValueError(f"{name}: the strides reach past the tensor's memory")
+
+
+def _here(*tensors) -> None:
+    """Kernels run on the current device; every buffer has to be there."""
+    import torch
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda:
+            raise ValueError("a tensor that is not on a CUDA device")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"a tensor on {t.device} while cuda:{torch.cuda.current_device()} is the current device")
+
+
+def _mx_pools(desc, layout, poolK, poolV) -> None:
+    n = loopvq_mx_pool_bytes(desc, layout.pool_tokens)
+    _want("poolK", poolK, ("uint8",), n)
+    _want("poolV", poolV, ("uint8",), n)
+
+
+def _mx_rows(desc, layout, first_step, n_steps, a, b, stride_t, stride_n, stride_h) -> None:
+    if a.dtype != b.dtype:
+        raise TypeError("k and v differ in type")
+    if min(n_steps, stride_t, stride_n, stride_h) >= 0 and layout.total_new > 0:
+        last = ((n_steps - 1) * stride_t + (layout.total_new - 1) * stride_n + (desc.n_heads_kv - 1) * stride_h
+                + desc.head_dim - 1)
+        _want_strided("k", a, last)
+        _want_strided("v", b, last)
+
+
+def _prepared(name, args, keep, stream):
+    """A zero-argument call of entry point ``name``; without a stream, on
+    torch's current one at the time of each call."""
+    fn = getattr(_lib, name)
+    at = None if stream is None else _stream(stream)
+
+    def call():
+        st = fn(*args, _stream(None) if at is None else at)
+        if st != LOOPVQ_OK:
+            raise LoopVQError(name, st)
+    call._keep = keep
+    return call
+
+
+def loopvq_mx_pool_bytes(desc, pool_tokens: int) -> int:
+    return _lib.loopvq_mx_pool_bytes(ctypes.byref(desc), pool_tokens)
+
+
+def prepare_mx_write(desc, layout, first_step, n_steps, k, v, stride_t, stride_n, stride_h, poolK, poolV,
+                     fault_bits=None, stream=None):
+    """loopvq_mx_write with every argument checked and marshalled once:
+    returns a zero-argument callable that issues the call.  The tensors must
+    stay in place; their contents may change between calls."""
+    _here(k, v, poolK, poolV, *layout._keep)
+    _mx_pools(desc, layout, poolK, poolV)
+    _mx_rows(desc, layout, first_step, n_steps, k, v, stride_t, stride_n, stride_h)
+    return _prepared("loopvq_mx_write", (
+        ctypes.byref(desc), ctypes.byref(layout), first_step, n_steps, _ptr(k), _ptr(v), _dtype_code(k), stride_t,
+        stride_n, stride_h, _ptr(poolK), _ptr(poolV), _ptr(fault_bits)),
+        (desc, layout, k, v, poolK, poolV, fault_bits), stream)
+
+
+def loopvq_mx_write(desc, layout, first_step, n_steps, k, v, stride_t, stride_n, stride_h, poolK, poolV,
+                    fault_bits=None, stream=None) -> None:
+    """Quantises the new tokens' keys and values of n_steps loop steps into
+    the pools."""
+    prepare_mx_write(desc, layout, first_step, n_steps, k, v, stride_t, stride_n, stride_h, poolK, poolV, fault_bits,
+                     stream)()
+
+
+def prepare_mx_read(desc, layout, first_step, n_steps, poolK, poolV, k_out, v_out, stride_t, stride_n, stride_h,
+                    fault_bits=None, stream=None):
+    """loopvq_mx_read, prepared as prepare_mx_write is."""
+    _here(k_out, v_out, poolK, poolV, *layout._keep)
+    _mx_pools(desc, layout, poolK, poolV)
+    _mx_rows(desc, layout, first_step, n_steps, k_out, v_out, stride_t, stride_n, stride_h)
+    return _prepared("loopvq_mx_read", (
+        ctypes.byref(desc), ctypes.byref(layout), first_step, n_steps, _ptr(poolK), _ptr(poolV), _ptr(k_out),
+        _ptr(v_out), _dtype_code(k_out), stride_t, stride_n, stride_h, _ptr(fault_bits)),
+        (desc, layout, k_out, v_out, poolK, poolV, fault_bits), stream)
+
+
+def loopvq_mx_read(desc, layout, first_step, n_steps, poolK, poolV, k_out, v_out, stride_t, stride_n, stride_h,
+                   fault_bits=None, stream=None) -> None:
+    """The values that the new tokens' codes stand for."""
+    prepare_mx_read(desc, layout, first_step, n_steps, poolK, poolV, k_out, v_out, stride_t, stride_n, stride_h,
+                    fault_bits, stream)()
+
+
+def loopvq_mx_attn_workspace_bytes(desc, layout) -> int:
+    return _lib.loopvq_mx_attn_workspace_bytes(ctypes.byref(desc), ctypes.byref(layout))
+
+
+def prepare_mx_attn(desc, layout, poolK, poolV, q, q_stride_n, q_stride_h, tree_mask, loop_step, softmax_scale,
+                    softcap, slopes, out, lse_out, workspace, fault_bits=None, stream=None):
+    """loopvq_mx_attn, prepared as prepare_mx_write is.  tree_mask: int64 or
+    uint64 [total_new], bit j of row i: new token i sees new token j."""
+    _here(q, out, lse_out, workspace, poolK, poolV, tree_mask, slopes, *layout._keep)
+    _mx_pools(desc, layout, poolK, poolV)
+    rows, Hq, D = max(0, layout.total_new), desc.n_heads_q, desc.head_dim
+    _want("tree_mask", tree_mask, ("int64", "uint64"), rows)
+    _want("slopes", slopes, ("float32",), Hq)
+    _want("out", out, ("float32", "bfloat16"), rows * Hq * D)
+    _want("lse_out", lse_out, ("float32",), rows * Hq)
+    if rows and q_stride_n >= 0 and q_stride_h >= 0:
+        _want_strided("q", q, (rows - 1) * q_stride_n + (Hq - 1) * q_stride_h + D - 1)
+    return _prepared("loopvq_mx_attn", (
+        ctypes.byref(desc), ctypes.byref(layout), _ptr(poolK), _ptr(poolV), _ptr(q), _dtype_code(q), q_stride_n,
+        q_stride_h, _ptr(tree_mask), loop_step, softmax_scale, softcap, _ptr(slopes), _ptr(out), _dtype_code(out),
+        _ptr(lse_out), _ptr(workspace), _nbytes(workspace), _ptr(fault_bits)),
+        (desc, layout, q, tree_mask, slopes, out, lse_out, workspace, poolK, poolV, fault_bits), stream)
+
+
+def loopvq_mx_attn(desc, layout, poolK, poolV, q, q_stride_n, q_stride_h, tree_mask, loop_step, softmax_scale,
+                   softcap, slopes, out, lse_out, workspace, fault_bits=None, stream=None) -> None:
+    """Attention of the new tokens (single ones, or trees of drafted ones)
+    over the coded contexts at one loop step."""
+    prepare_mx_attn(desc, layout, poolK, poolV, q, q_stride_n, q_stride_h, tree_mask, loop_step, softmax_scale,
+                    softcap, slopes, out, lse_out, workspace, fault_bits, stream)()
+
+
+def prepare_mx_keep(desc, layout, keep, n_keep, max_keep, poolK, poolV, fault_bits=None, stream=None):
+    """loopvq_mx_keep, prepared as prepare_mx_write is."""
+    _here(keep, n_keep, poolK, poolV, *layout._keep)
+    _mx_pools(desc, layout, poolK, poolV)
+    _want("keep", keep, ("int32",), layout.batch * max(0, max_keep))
+    _want("n_keep", n_keep, ("int32",), layout.batch)
+    return _prepared("loopvq_mx_keep", (
+        ctypes.byref(desc), ctypes.byref(layout), _ptr(keep), _ptr(n_keep), max_keep, _ptr(poolK), _ptr(poolV),
+        _ptr(fault_bits)), (desc, layout, keep, n_keep, poolK, poolV, fault_bits), stream)
+
+
+def loopvq_mx_keep(desc, layout, keep, n_keep, max_keep, poolK, poolV, fault_bits=None, stream=None) -> None:
+    """Moves the accepted drafts to the places after their prefix."""
+    prepare_mx_keep(desc, layout, keep, n_keep, max_keep, poolK, poolV, fault_bits, stream)()
 
 
 def loopvq_decode_workspace_bytes(desc, layout) -> int:
