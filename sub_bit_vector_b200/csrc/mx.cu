@@ -5,8 +5,8 @@
 // nearest to x * 2^-e.  Scaling by a power of two is exact, so the one
 // rounding is the conversion instruction's (nearest even).
 //
-// All three kernels move bytes; DRAM bounds them.  A warp owns one tile (32
-// tokens) of one head of K or V, because a tile's bytes interleave its tokens
+// The kernels move bytes; DRAM bounds them.  For many tokens a warp owns one
+// tile (32 tokens) of one head of K or V, because a tile's bytes interleave its tokens
 // the way the attention's matrix instructions take them: the lane that loads
 // a piece of a row in the order of the pool is the lane that stores it, in
 // 16-byte pieces, with no exchange but the block's maximum.  The warps of a
@@ -16,9 +16,13 @@
 namespace loopvq {
 namespace {
 
+// Up to so many new tokens of a request the kernels for a few tokens run.
+constexpr int kMxFew = 16;
+
 struct MxMoveParams {
   MxLayout L;
   int H, n_steps, first_step, head_groups;
+  bool few;
   int64_t st, sn, sh;
   const void *xk, *xv;   // write: in
   void *ok, *ov;         // read: out
@@ -378,135 +382,263 @@ __global__ void __launch_bounds__(256) mx_read_kernel(const MxMoveParams p) {
   }
 }
 
-// ------------------------------------------------------------------- keep
+// ------------------------------------------------------- a few tokens, keep
 //
-// A warp owns one head of K or V of one step of one request.  It takes the
-// (at most three) tiles that hold the request's new tokens into shared
-// memory, and only then writes the moved tokens from that copy: any order
-// of indices is safe, nothing is read after it was overwritten.
-constexpr int kMxKeepTiles = (kMxMaxTree + kMxTile - 2) / kMxTile + 1;
+// For a few tokens of each request a tile per warp would move 32 tokens' bytes
+// for one.  Here a lane holds 4 channels of the tokens of a quad (4 * i ..
+// 4 * i + 3 of a tile): the bytes of a quad that a lane reads or writes are its
+// own, so quads with old tokens are merged in registers without exchange.  A
+// warp covers 128 channels: one head (D = 128) or two (64), of K or of V.
+template <int D, int FMT>
+struct MxQuad {
+  using Tile = MxTile<D, FMT>;
+  uint8_t* tile;
+  int sub, c, b, l;   // half, quad of the half, block, lane within the block
+  __device__ __forceinline__ MxQuad(uint8_t* tile_, int quad, int lane)
+      : tile(tile_), sub(quad >> 2), c(quad & 3), b(lane % (D / 4) >> 3), l(lane & 7) {}
+  // K: the 4 codes of token t, 4 or 2 bytes
+  __device__ __forceinline__ uint8_t* key(int t) const {
+    const int per = Tile::kLaneBytes / 4;
+    return tile + mx_code_off<D, FMT>(sub, b, (2 * c + (t & 1)) * 4 + (l >> 1)) + ((t >> 1) * 2 + (l & 1)) * per;
+  }
+  __device__ __forceinline__ uint32_t load_key(int t) const {
+    if constexpr (FMT == LOOPVQ_MX_E4M3) return *reinterpret_cast<const uint32_t*>(key(t));
+    else return *reinterpret_cast<const uint16_t*>(key(t));
+  }
+  __device__ __forceinline__ void store_key(int t, uint32_t w) const {
+    if constexpr (FMT == LOOPVQ_MX_E4M3) *reinterpret_cast<uint32_t*>(key(t)) = w;
+    else *reinterpret_cast<uint16_t*>(key(t)) = (uint16_t)w;
+  }
+  // V: [channel j][token t], 16 or 8 bytes
+  __device__ __forceinline__ uint8_t* value() const { return tile + mx_code_off<D, FMT>(sub, b, l * 4 + c); }
+  __device__ __forceinline__ uint4 load_value() const {
+    if constexpr (FMT == LOOPVQ_MX_E4M3) return *reinterpret_cast<const uint4*>(value());
+    const uint2 w = *reinterpret_cast<const uint2*>(value());
+    return make_uint4(w.x, w.y, 0u, 0u);
+  }
+  __device__ __forceinline__ void store_value(uint4 w) const {
+    if constexpr (FMT == LOOPVQ_MX_E4M3) *reinterpret_cast<uint4*>(value()) = w;
+    else *reinterpret_cast<uint2*>(value()) = make_uint2(w.x, w.y);
+  }
+  // Codes of token t out of a value piece, as load_key gives them.
+  static __device__ __forceinline__ uint32_t token(uint4 w, int t) {
+    if constexpr (FMT == LOOPVQ_MX_E4M3) {
+      const uint32_t lo = __byte_perm(w.x, w.y, t | (4 + t) << 4), hi = __byte_perm(w.z, w.w, t | (4 + t) << 4);
+      return __byte_perm(lo, hi, 0x5410);
+    } else {
+      const uint32_t x = w.x >> (4 * t), y = w.y >> (4 * t);
+      return (x & 15u) | (x >> 16 & 15u) << 4 | (y & 15u) << 8 | (y >> 16 & 15u) << 12;
+    }
+  }
+  // A value piece with token t's codes put in.
+  static __device__ __forceinline__ uint4 with_token(uint4 w, int t, uint32_t v) {
+    if constexpr (FMT == LOOPVQ_MX_E4M3) {
+      const uint32_t keep = ~(0xffu << (8 * t));
+      w.x = (w.x & keep) | (v & 0xffu) << (8 * t);
+      w.y = (w.y & keep) | (v >> 8 & 0xffu) << (8 * t);
+      w.z = (w.z & keep) | (v >> 16 & 0xffu) << (8 * t);
+      w.w = (w.w & keep) | (v >> 24) << (8 * t);
+    } else {
+      const uint32_t keep = ~(0x000f000fu << (4 * t));
+      w.x = (w.x & keep) | ((v & 15u) | (v >> 4 & 15u) << 16) << (4 * t);
+      w.y = (w.y & keep) | ((v >> 8 & 15u) | (v >> 12 & 15u) << 16) << (4 * t);
+    }
+    return w;
+  }
+  // Scale byte of token t.
+  __device__ __forceinline__ uint8_t* scale(int t) const { return tile + mx_scale_off<D, FMT>(sub * 4 + c, b) + t; }
+};
+
+// What a lane of the kernels for a few tokens works on: head and kind.
+template <int D>
+struct MxFew {
+  MxReq q;
+  int kind, h;
+  bool there;
+  __device__ __forceinline__ MxFew(const MxLayout& L, int H, uint32_t* fault) {
+    constexpr int kHeads = 128 / D;
+    const int groups = (H + kHeads - 1) / kHeads;   // of one kind
+    const int w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    kind = w >= groups;
+    h = (w - kind * groups) * kHeads + (threadIdx.x & 31) / (D / 4);
+    there = w < 2 * groups && mx_request(L, blockIdx.z, &q, fault) && q.n > 0;   // uniform in the warp
+  }
+};
+
+template <int D, int FMT, typename T, bool VEC>
+__global__ void __launch_bounds__(256) mx_write_few_kernel(const MxMoveParams p) {
+  using Quad = MxQuad<D, FMT>;
+  const MxFew<D> u(p.L, p.H, p.fault);
+  if (!u.there) return;
+  const int lane = threadIdx.x & 31;
+  const bool in_h = u.h < p.H;
+  const T* x = reinterpret_cast<const T*>(u.kind ? p.xv : p.xk) + blockIdx.y * p.st + (in_h ? u.h : 0) * p.sh +
+               (int64_t)u.q.row0 * p.sn + 4 * (lane % (D / 4));
+  const int64_t stream = ((int64_t)(p.first_step + blockIdx.y) * p.H + (in_h ? u.h : 0)) * p.L.pool_tiles;
+  for (int quad = u.q.base >> 2; quad * 4 < u.q.ctx; ++quad) {
+    const int64_t pt = mx_pool_tile(p.L, blockIdx.z, quad >> 3, p.fault);
+    if (pt < 0) continue;
+    float v[4][4];
+    bool in[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int tok = quad * 4 + t;
+      in[t] = in_h && tok >= u.q.base && tok < u.q.ctx;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[t][j] = 0.f;
+      if (in[t]) load_channels<T, 4, VEC>(x + (int64_t)(tok - u.q.base) * p.sn, v[t]);
+    }
+    const Quad at((u.kind ? p.pv : p.pk) + (stream + pt) * MxTile<D, FMT>::kBytes, quad & 7, lane);
+    uint4 piece = {};
+    if (u.kind && in_h) piece = at.load_value();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = max(m, abs_bits(v[t][j]));
+#pragma unroll
+      for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+      if (!in[t]) continue;
+      float inv;
+      const uint32_t byte = mx_scale<FMT>(m, &inv);
+      const uint32_t code =
+          byte == kMxNan ? 0u : mx_codes4<FMT>(v[t][0] * inv, v[t][1] * inv, v[t][2] * inv, v[t][3] * inv);
+      if (u.kind) piece = Quad::with_token(piece, t, code);
+      else at.store_key(t, code);
+      if (at.l == 0) *at.scale(t) = (uint8_t)byte;
+    }
+    if (u.kind && in_h) at.store_value(piece);
+  }
+}
+
+template <int D, int FMT, typename T, bool VEC>
+__global__ void __launch_bounds__(256) mx_read_few_kernel(const MxMoveParams p) {
+  using Quad = MxQuad<D, FMT>;
+  const MxFew<D> u(p.L, p.H, p.fault);
+  if (!u.there || u.h >= p.H) return;
+  const int lane = threadIdx.x & 31;
+  T* x = reinterpret_cast<T*>(u.kind ? p.ov : p.ok) + blockIdx.y * p.st + u.h * p.sh + (int64_t)u.q.row0 * p.sn +
+         4 * (lane % (D / 4));
+  const int64_t stream = ((int64_t)(p.first_step + blockIdx.y) * p.H + u.h) * p.L.pool_tiles;
+#pragma unroll 2
+  for (int quad = u.q.base >> 2; quad < (u.q.ctx + 3) >> 2; ++quad) {
+    const int64_t pt = mx_pool_tile(p.L, blockIdx.z, quad >> 3, p.fault);
+    if (pt < 0) continue;
+    const Quad at((u.kind ? p.pv : p.pk) + (stream + pt) * MxTile<D, FMT>::kBytes, quad & 7, lane);
+    const uint32_t sc = *reinterpret_cast<const uint32_t*>(at.scale(0));
+    uint4 piece = {};
+    if (u.kind) piece = at.load_value();
+    uint32_t w[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int tok = quad * 4 + t;
+      if (tok < u.q.base || tok >= u.q.ctx) continue;
+      w[t] = u.kind ? Quad::token(piece, t) : at.load_key(t);
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int tok = quad * 4 + t;
+      if (tok < u.q.base || tok >= u.q.ctx) continue;
+      constexpr int kBits = FMT == LOOPVQ_MX_E4M3 ? 16 : 8;
+      const float2 a = mx_value2<FMT>(w[t] & ((1u << kBits) - 1)), b = mx_value2<FMT>(w[t] >> kBits);
+      const float s = mx_scale_value(sc >> (8 * t) & 255u);
+      const float v[4] = {a.x * s, a.y * s, b.x * s, b.y * s};
+      store_channels<T, 4, VEC>(x + (int64_t)(tok - u.q.base) * p.sn, v);
+    }
+  }
+}
+
+// Keep.  A warp takes all kept tokens' codes of its channels into shared
+// memory, and only then writes them to their places: any order of indices is
+// safe, nothing is read after it was overwritten.
+constexpr int kMxKeepTiles = (kMxMaxTree + kMxTile - 2) / kMxTile + 1;   // that 64 tokens can touch
 constexpr int kMxKeepWarps = 4;
 
 struct MxKeepParams {
   MxLayout L;
   int H;
   const int32_t *keep, *n_keep;
-  int max_keep;
+  int max_keep, room;   // row length of keep; tokens that the shared memory of a warp holds
   uint8_t *pk, *pv;
   uint32_t* fault;
 };
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeepParams p) {
-  using Tile = MxTile<D, FMT>;
-  constexpr int NB = Tile::kBlocks;
-  extern __shared__ __align__(16) uint8_t sm_all[];
-  __shared__ int16_t sm_src[kMxKeepWarps][kMxKeepTiles * kMxTile];   // by token - 32 * first tile
+  using Quad = MxQuad<D, FMT>;
+  extern __shared__ __align__(16) uint32_t sm_all[];   // per warp: codes [room][32], scales [room][4] bytes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* sm = sm_all + warp * kMxKeepTiles * Tile::kBytes;
-  int16_t* src = sm_src[warp];
-  const int hk = blockIdx.x * kMxKeepWarps + warp;
-  if (hk >= 2 * p.H) return;
-  const int r = blockIdx.z;
-  MxReq q;
-  if (!mx_request(p.L, r, &q, p.fault)) return;
-  const int nk = __ldg(p.n_keep + r);
-  if (nk < 0 || nk > q.n || nk > p.max_keep) {
+  uint32_t* code = sm_all + warp * p.room * 33;
+  uint8_t* scale = reinterpret_cast<uint8_t*>(code + p.room * 32);
+  const MxFew<D> u(p.L, p.H, p.fault);
+  if (!u.there) return;
+  const int r = blockIdx.z, nk = __ldg(p.n_keep + r);
+  if (nk < 0 || nk > u.q.n || nk > p.max_keep || nk > p.room) {
     set_fault(p.fault, LOOPVQ_FAULT_CTX_RANGE);
     return;
   }
   if (nk == 0) return;
-  const int t0 = q.base / kMxTile, org = t0 * kMxTile;
-  const int n_tiles = (q.ctx - 1) / kMxTile - t0 + 1;   // n <= 64: at most kMxKeepTiles
-  const int kind = hk >= p.H, h = hk - kind * p.H;
-  uint8_t* stream = (kind ? p.pv : p.pk) + ((int64_t)blockIdx.y * p.H + h) * p.L.pool_tiles * Tile::kBytes;
+  const bool in_h = u.h < p.H;
+  uint8_t* stream = (u.kind ? p.pv : p.pk) +
+                    ((int64_t)blockIdx.y * p.H + (in_h ? u.h : 0)) * p.L.pool_tiles * MxTile<D, FMT>::kBytes;
+  const int t0 = u.q.base / kMxTile;
   int64_t tile_at[kMxKeepTiles];
 #pragma unroll
-  for (int i = 0; i < kMxKeepTiles; ++i) {
-    tile_at[i] = i < n_tiles ? mx_pool_tile(p.L, r, t0 + i, p.fault) : -1;
-    if (tile_at[i] >= 0) {
-      const uint4* s = reinterpret_cast<const uint4*>(stream + tile_at[i] * Tile::kBytes);
-      for (int b = lane; b < Tile::kBytes / 16; b += 32) reinterpret_cast<uint4*>(sm + i * Tile::kBytes)[b] = s[b];
+  for (int i = 0; i < kMxKeepTiles; ++i)
+    tile_at[i] = (t0 + i) * kMxTile < u.q.ctx ? mx_pool_tile(p.L, r, t0 + i, p.fault) : -1;
+  auto tile_of = [&](int pos) {
+    const int i = pos / kMxTile - t0;
+    return i == 0 ? tile_at[0] : i == 1 ? tile_at[1] : tile_at[2];
+  };
+  // sources of tokens lane and lane + 32 (-1: the token stays as it is)
+  int from[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = lane + 32 * k;
+    from[k] = -1;
+    if (i < nk) {
+      const int f = __ldg(p.keep + (int64_t)r * p.max_keep + i);
+      if (f < 0 || f >= u.q.n) set_fault(p.fault, LOOPVQ_FAULT_CTX_RANGE);
+      else if (f != i && tile_of(u.q.base + f) >= 0) from[k] = f;
     }
   }
-  // where each token of these tiles comes from (-1: it stays)
-  for (int i = lane; i < kMxKeepTiles * kMxTile; i += 32) {
-    const int k = org + i - q.base;
-    int from = -1;
-    if (k >= 0 && k < nk) {
-      const int f = __ldg(p.keep + (int64_t)r * p.max_keep + k);
-      if (f < 0 || f >= q.n) {
-        set_fault(p.fault, LOOPVQ_FAULT_CTX_RANGE);
-      } else if (f != k) {
-        from = q.base + f - org;
-        if (mx_pool_tile(p.L, r, t0 + from / kMxTile, p.fault) < 0) from = -1;
-      }
-    }
-    src[i] = (int16_t)from;
+#pragma unroll 4
+  for (int i = 0; i < nk; ++i) {
+    const int f = __shfl_sync(0xffffffffu, i < 32 ? from[0] : from[1], i & 31);
+    if (f < 0 || !in_h) continue;
+    const int pos = u.q.base + f;
+    const Quad at(stream + tile_of(pos) * MxTile<D, FMT>::kBytes, (pos >> 2) & 7, lane);
+    code[i * 32 + lane] = u.kind ? Quad::token(at.load_value(), pos & 3) : at.load_key(pos & 3);
+    if (at.l == 0) scale[i * 4 + (lane >> 3)] = *at.scale(pos & 3);
   }
+  const uint32_t moved[2] = {__ballot_sync(0xffffffffu, from[0] >= 0), __ballot_sync(0xffffffffu, from[1] >= 0)};
   __syncwarp();
-  const int last = q.base + nk - 1 - org;   // last token written
+  if (!in_h) return;
+  for (int quad = u.q.base >> 2; quad * 4 < u.q.base + nk; ++quad) {
+    const int64_t pt = tile_of(quad * 4);
+    if (pt < 0) continue;
+    const Quad at(stream + pt * MxTile<D, FMT>::kBytes, quad & 7, lane);
+    uint4 piece = {};
+    if (u.kind) piece = at.load_value();
+    bool any = false;
 #pragma unroll
-  for (int i = 0; i < kMxKeepTiles; ++i) {
-    if (tile_at[i] < 0 || i * kMxTile > last) continue;
-    uint8_t* out = stream + tile_at[i] * Tile::kBytes;
-    if (kind == LOOPVQ_KEYS) {
-      // a piece: 8 channels of one token (8 or 4 bytes)
-      constexpr int kPiece = Tile::kLaneBytes / 2;
-      for (int e = lane; e < kMxTile * NB * 4; e += 32) {
-        const int cc = e & 3, b = (e >> 2) % NB, n = e / (4 * NB), f = src[i * kMxTile + n];
-        if (f < 0) continue;
-        auto off = [&](int m) {
-          const int gg = ((m & 15) >> 2) * 2 + (m & 1), ab = m >> 1 & 1;
-          return mx_code_off<D, FMT>(m >> 4 & 1, b, gg * 4 + cc) + ab * kPiece;
-        };
-        const uint8_t* s = sm + (f / kMxTile) * Tile::kBytes + off(f % kMxTile);
-        uint8_t* d = out + off(n);
-        if constexpr (kPiece == 8) *reinterpret_cast<uint2*>(d) = *reinterpret_cast<const uint2*>(s);
-        else *reinterpret_cast<uint32_t*>(d) = *reinterpret_cast<const uint32_t*>(s);
-      }
-    } else {
-      // a word: four tokens of one channel (e4m3) or of two (e2m1); the tokens
-      // that stay keep their bits, which this warp alone may write
-      constexpr int kWords = Tile::kLaneBytes / 4;   // of a lane and block
-      for (int e = lane; e < 8 * NB * 8 * kWords; e += 32) {
-        const int j = e % kWords, gg = e / kWords % 8, b = e / (kWords * 8) % NB, quad = e / (kWords * 8 * NB);
-        auto off = [&](int m) { return mx_code_off<D, FMT>(m >> 4 & 1, b, gg * 4 + (m >> 2 & 3)) + j * 4; };
-        const int16_t* qs = src + i * kMxTile + quad * 4;
-        uint32_t mask = 0, bits = 0;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int f = qs[t];
-          if (f < 0) continue;
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(sm + (f / kMxTile) * Tile::kBytes + off(f % kMxTile));
-          if constexpr (FMT == LOOPVQ_MX_E4M3) {
-            mask |= 0xffu << (8 * t);
-            bits |= (w >> (8 * (f & 3)) & 0xffu) << (8 * t);
-          } else {
-            mask |= 0x000f000fu << (4 * t);
-            bits |= (w >> (4 * (f & 3)) & 0x000f000fu) << (4 * t);
-          }
-        }
-        if (mask) {
-          const uint32_t old = *reinterpret_cast<const uint32_t*>(sm + i * Tile::kBytes + off(quad * 4));
-          *reinterpret_cast<uint32_t*>(out + off(quad * 4)) = (old & ~mask) | bits;
-        }
-      }
+    for (int t = 0; t < 4; ++t) {
+      const int i = quad * 4 + t - u.q.base;
+      if (i < 0 || i >= nk || !(moved[i >> 5] >> (i & 31) & 1)) continue;
+      any = true;
+      const uint32_t w = code[i * 32 + lane];
+      if (u.kind) piece = Quad::with_token(piece, t, w);
+      else at.store_key(t, w);
+      if (at.l == 0) *at.scale(t) = scale[i * 4 + (lane >> 3)];
     }
-    for (int e = lane; e < 8 * NB; e += 32) {   // scale words: four tokens of one block
-      const int b = e % NB, quad = e / NB;
-      const uint32_t old = *reinterpret_cast<const uint32_t*>(sm + i * Tile::kBytes + mx_scale_off<D, FMT>(quad, b));
-      uint32_t now = old;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int f = src[i * kMxTile + quad * 4 + t];
-        if (f < 0) continue;
-        const int at = (f / kMxTile) * Tile::kBytes + mx_scale_off<D, FMT>(f % kMxTile >> 2, b);
-        now = (now & ~(0xffu << (8 * t))) | (uint32_t)sm[at + (f & 3)] << (8 * t);
-      }
-      if (now != old) *reinterpret_cast<uint32_t*>(out + mx_scale_off<D, FMT>(quad, b)) = now;
-    }
+    if (u.kind && any) at.store_value(piece);
   }
+}
+
+// Blocks of `warps` warps over the heads of K and V.
+unsigned few_blocks(const loopvq_mx_desc* d, int warps) {
+  const int heads = 128 / d->head_dim, groups = (d->n_heads_kv + heads - 1) / heads;
+  return (unsigned)((2 * groups + warps - 1) / warps);
 }
 
 loopvq_status move_setup(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout, int32_t first_step,
@@ -536,6 +668,8 @@ loopvq_status move_setup(const loopvq_mx_desc* desc, const loopvq_mx_layout* lay
   const int64_t x = tiles * p->head_groups;
   if (x > 0x7fffffffLL || n_steps > 65535) return LOOPVQ_ERR_UNSUPPORTED;
   *grid = dim3((unsigned)x, (unsigned)n_steps, (unsigned)p->L.batch);
+  p->few = p->L.max_new <= kMxFew;
+  if (p->few) grid->x = few_blocks(desc, 8);
   return LOOPVQ_OK;
 }
 // Vector loads and stores of 8 bf16 or 4 fp32 channels.
@@ -624,7 +758,8 @@ extern "C" loopvq_status loopvq_mx_write(const loopvq_mx_desc* desc, const loopv
   if (!k || !v || (uintptr_t)k % es || (uintptr_t)v % es) return LOOPVQ_ERR_INVALID_ARG;
   p.xk = k;
   p.xv = v;
-  MX_MOVE(mx_write_kernel, x_dtype, k, v);
+  if (p.few) MX_MOVE(mx_write_few_kernel, x_dtype, k, v);
+  else MX_MOVE(mx_write_kernel, x_dtype, k, v);
   return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }
 
@@ -647,7 +782,8 @@ extern "C" loopvq_status loopvq_mx_read(const loopvq_mx_desc* desc, const loopvq
     return LOOPVQ_ERR_INVALID_ARG;
   p.ok = k_out;
   p.ov = v_out;
-  MX_MOVE(mx_read_kernel, out_dtype, k_out, v_out);
+  if (p.few) MX_MOVE(mx_read_few_kernel, out_dtype, k_out, v_out);
+  else MX_MOVE(mx_read_kernel, out_dtype, k_out, v_out);
   return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }
 
@@ -671,13 +807,12 @@ extern "C" loopvq_status loopvq_mx_keep(const loopvq_mx_desc* desc, const loopvq
   p.pk = (uint8_t*)poolK;
   p.pv = (uint8_t*)poolV;
   p.fault = fault_bits;
-  const dim3 grid((2 * p.H + kMxKeepWarps - 1) / kMxKeepWarps, desc->n_loop, p.L.batch);
-  const size_t smem = kMxKeepWarps * kMxKeepTiles * mx_tile_bytes(desc->head_dim, desc->format);
+  const dim3 grid(few_blocks(desc, kMxKeepWarps), desc->n_loop, p.L.batch);
+  p.room = max_keep < layout->max_new ? max_keep : layout->max_new;
+  const size_t smem = (size_t)kMxKeepWarps * p.room * 33 * sizeof(uint32_t);   // at most 33,792 bytes
   auto kfn = desc->head_dim == 128
                  ? (desc->format == LOOPVQ_MX_E4M3 ? mx_keep_kernel<128, LOOPVQ_MX_E4M3> : mx_keep_kernel<128, LOOPVQ_MX_E2M1>)
                  : (desc->format == LOOPVQ_MX_E4M3 ? mx_keep_kernel<64, LOOPVQ_MX_E4M3> : mx_keep_kernel<64, LOOPVQ_MX_E2M1>);
-  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return LOOPVQ_ERR_CUDA;
   kfn<<<grid, kMxKeepWarps * 32, smem, (cudaStream_t)stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }

@@ -36,12 +36,13 @@ constexpr int kAttnWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kScoreSlack = 10.f, kWeightMax = 32768.f, kWeightExp = 8.f;
 
-template <int D, int FMT>
+template <int D, int FMT, int NARROW, int NT>
 struct MxRing {
-  static constexpr int kStages = 3;
   static constexpr int kSlot = 2 * MxTile<D, FMT>::kBytes;   // K tile, V tile
+  static constexpr int kStages = kSlot > 8000 ? 2 : 3;
   static constexpr int kBytes = kAttnWarps * kStages * kSlot;
-  static constexpr int kCtas = 200 * 1024 / kBytes < 4 ? 200 * 1024 / kBytes : 4;   // per SM
+  static constexpr int kMost = NARROW ? 4 : (D == 128 ? 4 : 5) - NT;   // by registers
+  static constexpr int kCtas = 216 * 1024 / kBytes < kMost ? 216 * 1024 / kBytes : kMost;   // per SM
 };
 
 struct MxAttnParams {
@@ -58,7 +59,7 @@ struct MxAttnParams {
   int out_bf16;
   float* lse;
   int4* headers;     // per warp: the unit that starts in it and goes on
-  float* partials;   // per warp: 2 slots (a unit that began earlier; one that goes on) of [8 NT][D + 4]
+  float* partials;   // per warp: 2 slots (a unit that began earlier; one that goes on) of [chunk][D + 4]
   int min_tiles;     // least tiles of a warp
   uint32_t* fault;
 };
@@ -68,12 +69,42 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
-                                        const uint32_t a3, const uint32_t b0, const uint32_t b1) {
+// tanh y = 1 - 2 / (1 + e^2y), right to 2^-23 absolutely, which is what a score needs.
+__device__ __forceinline__ float tanh_abs(float y) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(2.f * kLog2e * y)));
+  return fmaf(-2.f, r, 1.f);
+}
+// d = a (16 x 16) b (16 x 8) + c
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                        const float (&c)[4]) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+__device__ __forceinline__ uint64_t pair(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
+  return unpair(r);
+}
+__device__ __forceinline__ void fma2(float* c, float2 a, float2 b) {   // c[0..1] += a * b
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(make_float2(c[0], c[1]))));
+  const float2 v = unpair(r);
+  c[0] = v.x;
+  c[1] = v.y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
@@ -103,26 +134,45 @@ __device__ __forceinline__ uint32_t drop_nan_codes(uint32_t w) {
   return w & ~((m >> 7) * 0xffu);
 }
 
+// Rows of a request that one warp takes together, as NT groups of columns of
+// the second product.
+//   NARROW 0: a column is a query row; a lane goes through all blocks.
+//   NARROW 1: a column is a (query row, block of channels), so that a lane
+//             scales, exponentiates and packs weights for one block only.
+//   NARROW 2: a column is a (half of the tile, query row, block): one such
+//             pass covers both halves.  The halves are summed at the end as
+//             two parts of a split context.
+// Measured on 32 requests of 6-18K tokens, one row each, e2m1, D = 128: kind 0
+// 249 us, kind 1 181 us, kind 2 161 us.
+template <int D, int NARROW>
+struct MxRows {
+  static constexpr int kPerGroup = NARROW ? 8 / (D / kMxBlock) / NARROW : 8;
+};
+
 // Where in the list of tiles a warp is.
 struct MxCursor {
   int r, u, units, t, tiles;   // request, unit of its H * chunks, tile of its ctx
 };
 // Units and tiles of request r (0 units if it has no part in the call).
-template <int NT>
+template <int CHUNK>
 __device__ __forceinline__ int mx_units(const MxAttnParams& p, int r, int* tiles) {
   MxReq q;
   *tiles = 0;
   if (!mx_request(p.L, r, &q, p.fault) || q.n == 0 || q.n > kMxMaxTree) return 0;
   *tiles = (q.ctx + kMxTile - 1) / kMxTile;
-  return (q.n * p.G + 8 * NT - 1) / (8 * NT) * p.H;
+  return (q.n * p.G + CHUNK - 1) / CHUNK * p.H;
 }
-// The cursor at tile `at` of the whole list (0 <= at < total); uniform in the warp.
-template <int NT>
-__device__ __forceinline__ MxCursor mx_seek(const MxAttnParams& p, int64_t at, int lane) {
+// The cursor at tile `at` of the whole list (0 <= at < total); uniform in the
+// warp.  u0, t0: units and tiles of request `lane`.
+template <int CHUNK>
+__device__ __forceinline__ MxCursor mx_seek(const MxAttnParams& p, int64_t at, int u0, int t0, int lane) {
   MxCursor c = {0, 0, 0, 0, 1};
   for (int r0 = 0; r0 < p.L.batch; r0 += 32) {
-    int tiles = 0, units = 0;
-    if (r0 + lane < p.L.batch) units = mx_units<NT>(p, r0 + lane, &tiles);
+    int tiles = t0, units = u0;
+    if (r0) {
+      units = tiles = 0;
+      if (r0 + lane < p.L.batch) units = mx_units<CHUNK>(p, r0 + lane, &tiles);
+    }
     int64_t sum = (int64_t)units * tiles;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -146,7 +196,7 @@ __device__ __forceinline__ MxCursor mx_seek(const MxAttnParams& p, int64_t at, i
 }
 // On to the next unit; the caller knows that there is one (lengths that
 // change under the kernel are the caller's error; indices stay in range).
-template <int NT>
+template <int CHUNK>
 __device__ __forceinline__ void mx_next_unit(const MxAttnParams& p, MxCursor* c) {
   c->t = 0;
   if (++c->u < c->units) return;
@@ -158,28 +208,37 @@ __device__ __forceinline__ void mx_next_unit(const MxAttnParams& p, MxCursor* c)
       c->tiles = 1;
       return;
     }
-    c->units = mx_units<NT>(p, c->r, &c->tiles);
+    c->units = mx_units<CHUNK>(p, c->r, &c->tiles);
   } while (c->units == 0);
 }
 
-template <int D, int FMT, int TERMS, int NT>
-__global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_attn_kernel(const MxAttnParams p) {
+template <int D, int FMT, int NARROW, int TERMS, int NT>
+__global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::kCtas) mx_attn_kernel(const MxAttnParams p) {
   using Tile = MxTile<D, FMT>;
-  using Ring = MxRing<D, FMT>;
+  using Ring = MxRing<D, FMT, NARROW, NT>;
   constexpr int NB = Tile::kBlocks, S = Ring::kStages;
+  constexpr int RPG = MxRows<D, NARROW>::kPerGroup, CHUNK = RPG * NT;
   constexpr int MT = TERMS == 2 ? NT : (NT + 1) / 2;   // 16-row operands of the score product
-  constexpr int kHalves = TERMS == 1 && NT == 1 ? 1 : 2;
+  constexpr bool kBoth = TERMS == 2 || NT > 1;         // both halves of the 16 rows are used
+  constexpr int NW = NARROW ? 1 : NB;                  // blocks that a lane weighs
   extern __shared__ __align__(128) uint8_t sm_ring[];
   __shared__ __align__(8) uint64_t bars[kAttnWarps][S];
+  __shared__ __align__(16) float sm_scale[NARROW ? 1 : kAttnWarps][2][NARROW ? 4 : 32 * NB];   // of the tile: K, V
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  constexpr int SUBS = NARROW == 2 ? 2 : 1;            // halves of a tile that are in flight together
+  const int gb = NARROW ? g % NB : 0;                  // this lane's block,
+  const int gr = NARROW ? g / NB % RPG : g;            // row in a group,
+  const int half = NARROW == 2 ? g >> 2 : 0;           // half of the tile (NARROW 2)
   const int n_warps = gridDim.x * kAttnWarps, wid = blockIdx.x * kAttnWarps + warp;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // this warp's share of the list
-  int64_t total = 0;
-  for (int r = lane; r < p.L.batch; r += 32) {
+  int u0 = 0, t0 = 0;
+  if (lane < p.L.batch) u0 = mx_units<CHUNK>(p, lane, &t0);
+  int64_t total = (int64_t)u0 * t0;
+  for (int r = lane + 32; r < p.L.batch; r += 32) {
     int tiles;
-    const int units = mx_units<NT>(p, r, &tiles);
+    const int units = mx_units<CHUNK>(p, r, &tiles);
     total += (int64_t)units * tiles;
   }
 #pragma unroll
@@ -199,21 +258,24 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
   __syncwarp();
   uint8_t* ring = sm_ring + warp * S * Ring::kSlot;
 
-  MxCursor cc = mx_seek<NT>(p, begin, lane);   // consumer
-  MxCursor pc = cc;                            // producer
+  MxCursor cc = mx_seek<CHUNK>(p, begin, u0, t0, lane);   // consumer
+  MxCursor pc = cc;                                       // producer
   const int per = p.L.page_tokens / kMxTile;
   int page = pc.t / per, in_page = pc.t % per, issued = 0;
   uint32_t bad = 0;   // bit per slot: its tile's page is not in the pool
-  auto page_id = [&]() { return __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page); };
-  int id = page_id();
+  int id = 0;         // the page of the producer's tile
+  int64_t head = 0;   // first tile of its head
+  auto enter_unit = [&]() { head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles; };
+  auto enter_page = [&]() { id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page); };
+  enter_unit();
+  enter_page();
   auto issue = [&](int slot) {
     const bool ok = id >= 0 && id < p.L.n_pages;
     bad = (bad & ~(1u << slot)) | (ok ? 0u : 1u << slot);
     if (lane == 0) {
       const uint32_t bar = smem_u32(&bars[warp][slot]);
       if (ok) {
-        const int chunks = pc.units / p.H;
-        const int64_t at = ((int64_t)(pc.u / chunks) * p.L.pool_tiles + (int64_t)id * per + in_page) * Tile::kBytes;
+        const int64_t at = (head + (int64_t)id * per + in_page) * Tile::kBytes;
         const uint32_t dst = smem_u32(ring + slot * Ring::kSlot);
         mbar_arrive_expect_tx(bar, 2 * Tile::kBytes);
         bulk_g2s(dst, p.pk + at, Tile::kBytes, bar);
@@ -225,13 +287,14 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
     }
     if (++issued < count) {
       if (++pc.t == pc.tiles) {
-        mx_next_unit<NT>(p, &pc);
+        mx_next_unit<CHUNK>(p, &pc);
         page = in_page = 0;
-        id = page_id();
+        enter_unit();
+        enter_page();
       } else if (++in_page == per) {
         in_page = 0;
         ++page;
-        id = page_id();
+        enter_page();
       }
     }
   };
@@ -244,30 +307,30 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
     // ------------------------------------------------ a unit, or the part of it in this share
     MxReq rq = {};
     mx_request(p.L, cc.r, &rq, nullptr);
-    const int chunks = cc.units / p.H, h = cc.u / chunks, rho0 = (cc.u - h * chunks) * (8 * NT);
-    const int rows = min(8 * NT, rq.n * p.G - rho0);
+    const int chunks = cc.units / p.H, h = cc.u / chunks, rho0 = (cc.u - h * chunks) * CHUNK;
+    const int rows = min(CHUNK, rq.n * p.G - rho0);
     const int first_tile = cc.t, n_tiles = min(cc.tiles - cc.t, count - done);
     const uint64_t all_new = rq.n >= 64 ? ~0ull : (1ull << rq.n) - 1;
 
-    // query rows: scaled by a power of two to a largest magnitude in [2^14, 2^15), as fp16 (TERMS = 2: and the rest)
+    // query rows: scaled by a power of two (NARROW: of each block) to a largest
+    // magnitude in [2^14, 2^15), as fp16 (TERMS = 2: and the rest)
     uint32_t qa[MT][NB][2][4] = {};
     float f[NT], slope[NT];
     uint64_t sees[NT];
     int pos_q[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      const int rho = rho0 + 8 * i + g;
+      const int rho = rho0 + RPG * i + gr;
       f[i] = slope[i] = 0.f;
       sees[i] = 0;
       pos_q[i] = 0;
-      float v[NB][8];
+      float v[NW][8] = {};
       float mx = 0.f;
-      const bool there = rho < rq.n * p.G;
-      if (there) {
+      if (rho < rq.n * p.G) {
         const int node = rho / p.G, hq = h * p.G + rho % p.G;
-        const int64_t at = (int64_t)(rq.row0 + node) * p.qn + (int64_t)hq * p.qh + 8 * c;
+        const int64_t at = (int64_t)(rq.row0 + node) * p.qn + (int64_t)hq * p.qh + 32 * gb + 8 * c;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < NW; ++b) {
           if (p.q_bf16) {
             const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(p.q) + at + 32 * b;
             if (p.q_vec) {
@@ -289,15 +352,9 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
         sees[i] = (p.tree_mask ? __ldg(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
         pos_q[i] = rq.base + __popcll(sees[i] & ~(1ull << node));
         if (p.slopes) slope[i] = __ldg(p.slopes + hq) * kLog2e;
-      } else {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[b][k] = 0.f;
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // 2^k: mx = frac * 2^ex, ex the exponent field's value (subnormals count as the least)
       const int ex = max((int)(__float_as_uint(mx) >> 23), 1) - 127;
       const int k2 = min(14 - ex, 120);
       const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
@@ -306,26 +363,28 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float x0 = v[b][2 * k] * up, x1 = v[b][2 * k + 1] * up;
+          const int vb = NARROW ? 0 : b;
+          const bool has = !NARROW || gb == b;   // NARROW: a row of block b is 0 elsewhere
+          const float x0 = v[vb][2 * k] * up, x1 = v[vb][2 * k + 1] * up;
           const uint32_t hi = pack_f16(x0, x1);
           // pair k: channels 8c + 2k, 8c + 2k + 1: product k/2, upper half of its 16 channels if k is odd
           if constexpr (TERMS == 1) {
-            qa[i / 2][b][k >> 1][(k & 1) * 2 + (i & 1)] = hi;
+            qa[i / 2][b][k >> 1][(k & 1) * 2 + (i & 1)] = has ? hi : 0u;
           } else {
             const float2 b2 = unpack_f16(hi);
-            qa[i][b][k >> 1][(k & 1) * 2] = hi;
-            qa[i][b][k >> 1][(k & 1) * 2 + 1] = pack_f16(x0 - b2.x, x1 - b2.y);
+            qa[i][b][k >> 1][(k & 1) * 2] = has ? hi : 0u;
+            qa[i][b][k >> 1][(k & 1) * 2 + 1] = has ? pack_f16(x0 - b2.x, x1 - b2.y) : 0u;
           }
         }
     }
 
-    float m[NT], l[NT], M[NT][NB], rs[NT][NB], o[NB][2][NT][4];
+    float m[NT], l[NT], M[NT][NW], rs[NT][NW], o[NW][2][NT][4];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
+      for (int b = 0; b < NW; ++b) {
         M[i][b] = -INFINITY;
         rs[i][b] = 0.f;
 #pragma unroll
@@ -345,74 +404,115 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
       const int tok0 = (first_tile + it) * kMxTile;
       const bool edge = tok0 + kMxTile > rq.base;
       if (!(bad >> slot & 1)) {
-#pragma unroll 1
-        for (int sub = 0; sub < 2; ++sub) {
-          // ---- scores
-          float s[MT][2][4] = {};
-          uint32_t scw[NB];
-          {
-            const uint8_t* z = sk + mx_scale_off<D, FMT>(sub * 4 + c, 0);
-            if constexpr (NB == 4) {
-              const uint4 w = *reinterpret_cast<const uint4*>(z);
-              scw[0] = w.x; scw[1] = w.y; scw[2] = w.z; scw[3] = w.w;
-            } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(z);
-              scw[0] = w.x; scw[1] = w.y;
+        if constexpr (!NARROW) {   // the tile's scales as fp32, once for all rows
+          if (lane < 8 * NB) {
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+              const uint32_t w = reinterpret_cast<const uint32_t*>((kv ? sv : sk) + Tile::kScaleOff)[lane];
+              reinterpret_cast<float4*>(sm_scale[warp][kv])[lane] =
+                  make_float4(scale_f32(w, 0), scale_f32(w, 1), scale_f32(w, 2), scale_f32(w, 3));
             }
           }
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int sub = 0; sub < 2; sub += SUBS) {
+          const int quad = (sub + half) * 4 + c;   // this lane's tokens: 4 * quad ..
+          // ---- scores
+          float s[SUBS][MT][2][4] = {};
+          float2 ksc[2];   // NARROW: this lane's block and tokens
+          if constexpr (NARROW) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(sk + mx_scale_off<D, FMT>(quad, gb));
+            ksc[0] = make_float2(scale_f32(w, 0), scale_f32(w, 1));
+            ksc[1] = make_float2(scale_f32(w, 2), scale_f32(w, 3));
+          }
 #pragma unroll
-          for (int b = 0; b < NB; b += 2) {
-            uint32_t h[2][2][4];   // [block][ab][pair]
-            if constexpr (FMT == LOOPVQ_MX_E4M3) {
+          for (int b = 0; b < NB; b += 2)
+#pragma unroll
+            for (int su = 0; su < SUBS; ++su) {
+              uint32_t hc[2][2][4];   // [block][ab][pair]
+              if constexpr (FMT == LOOPVQ_MX_E4M3) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint4 w = *reinterpret_cast<const uint4*>(sk + mx_code_off<D, FMT>(sub + su, b + k, lane));
+                  codes_e4m3(w.x, hc[k][0]);
+                  codes_e4m3(w.y, hc[k][0] + 2);
+                  codes_e4m3(w.z, hc[k][1]);
+                  codes_e4m3(w.w, hc[k][1] + 2);
+                }
+              } else {
+                const uint4 w = *reinterpret_cast<const uint4*>(sk + mx_code_off<D, FMT>(sub + su, b, lane));
+                codes_e2m1(w.x, hc[0][0]);
+                codes_e2m1(w.y, hc[0][1]);
+                codes_e2m1(w.z, hc[1][0]);
+                codes_e2m1(w.w, hc[1][1]);
+              }
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint4 w = *reinterpret_cast<const uint4*>(sk + mx_code_off<D, FMT>(sub, b + k, lane));
-                codes_e4m3(w.x, h[k][0]);
-                codes_e4m3(w.y, h[k][0] + 2);
-                codes_e4m3(w.z, h[k][1]);
-                codes_e4m3(w.w, h[k][1] + 2);
-              }
-            } else {
-              const uint4 w = *reinterpret_cast<const uint4*>(sk + mx_code_off<D, FMT>(sub, b, lane));
-              codes_e2m1(w.x, h[0][0]);
-              codes_e2m1(w.y, h[0][1]);
-              codes_e2m1(w.z, h[1][0]);
-              codes_e2m1(w.w, h[1][1]);
-            }
+                float4 sc = {};
+                if constexpr (!NARROW)
+                  sc = reinterpret_cast<const float4*>(sm_scale[NARROW ? 0 : warp][0])[quad * NB + b + k];
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+                for (int ab = 0; ab < 2; ++ab) {
 #pragma unroll
-              for (int ab = 0; ab < 2; ++ab) {
-                const float s0 = scale_f32(scw[b + k], 2 * ab), s1 = scale_f32(scw[b + k], 2 * ab + 1);
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                  float d[4] = {0.f, 0.f, 0.f, 0.f};
-                  const uint32_t(*a)[4] = qa[i][b + k];
-                  mma_f16(d, a[0][0], a[0][1], a[0][2], a[0][3], h[k][ab][0], h[k][ab][1]);
-                  mma_f16(d, a[1][0], a[1][1], a[1][2], a[1][3], h[k][ab][2], h[k][ab][3]);
-                  s[i][ab][0] = fmaf(d[0], s0, s[i][ab][0]);
-                  s[i][ab][1] = fmaf(d[1], s1, s[i][ab][1]);
-                  if constexpr (kHalves == 2) {
-                    s[i][ab][2] = fmaf(d[2], s0, s[i][ab][2]);
-                    s[i][ab][3] = fmaf(d[3], s1, s[i][ab][3]);
+                  for (int i = 0; i < MT; ++i) {
+                    const uint32_t(*a)[4] = qa[i][b + k];
+                    if constexpr (NARROW) {
+                      mma_f16(s[su][i][ab], a[0], hc[k][ab][0], hc[k][ab][1], s[su][i][ab]);
+                      mma_f16(s[su][i][ab], a[1], hc[k][ab][2], hc[k][ab][3], s[su][i][ab]);
+                    } else {
+                      const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                      float d[4];
+                      mma_f16(d, a[0], hc[k][ab][0], hc[k][ab][1], zero);
+                      mma_f16(d, a[1], hc[k][ab][2], hc[k][ab][3], d);
+                      const float2 s2 = ab ? make_float2(sc.z, sc.w) : make_float2(sc.x, sc.y);
+                      fma2(&s[su][i][ab][0], make_float2(d[0], d[1]), s2);
+                      if constexpr (kBoth) fma2(&s[su][i][ab][2], make_float2(d[2], d[3]), s2);
+                    }
                   }
                 }
               }
-          }
-          // ---- in log2 units, with cap, bias and mask: row g of group i, tokens 4c + t
-          const int pos = tok0 + 16 * sub + 4 * c;
+            }
+          // ---- in log2 units, with cap, bias and mask: row gr of group i, tokens 4c + t
+          const int pos = tok0 + 4 * quad;
           float x[NT][4];
           uint32_t hide = 0;   // bit 4i + t: not seen
 #pragma unroll
-          for (int i = 0; i < NT; ++i)
+          for (int i = 0; i < NT; ++i) {
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              float y = TERMS == 2 ? s[i % MT][t >> 1][t & 1] + s[i % MT][t >> 1][2 + (t & 1)]
-                                   : s[i / 2][t >> 1][2 * (i & 1) + (t & 1)];
-              y *= f[i];
-              if (p.softcap > 0.f) y = p.softcap * kLog2e * tanhf(y);
-              x[i][t] = y;
+            for (int ab = 0; ab < 2; ++ab) {
+              float2 y;
+              if constexpr (NARROW == 2) {   // rows g and g ^ 4 are the same query and block: this lane keeps its half of the tile
+                y = half ? make_float2(s[SUBS - 1][i / 2][ab][0], s[SUBS - 1][i / 2][ab][1])
+                         : make_float2(s[0][i / 2][ab][0], s[0][i / 2][ab][1]);
+                if constexpr (TERMS == 2) {
+                  y.x += half ? s[SUBS - 1][i / 2][ab][2] : s[0][i / 2][ab][2];
+                  y.y += half ? s[SUBS - 1][i / 2][ab][3] : s[0][i / 2][ab][3];
+                }
+              } else if constexpr (TERMS == 2) {
+                y = make_float2(s[0][i % MT][ab][0] + s[0][i % MT][ab][2], s[0][i % MT][ab][1] + s[0][i % MT][ab][3]);
+              } else {
+                y = make_float2(s[0][i / 2][ab][2 * (i & 1)], s[0][i / 2][ab][2 * (i & 1) + 1]);
+              }
+              y = mul2(y, make_float2(f[i], f[i]));
+              if constexpr (NARROW) {   // scaled, and summed over the blocks
+                y = mul2(y, ksc[ab]);
+#pragma unroll
+                for (int d = 4; d < 4 * NB; d <<= 1) {
+                  y.x += __shfl_xor_sync(0xffffffffu, y.x, d);
+                  y.y += __shfl_xor_sync(0xffffffffu, y.y, d);
+                }
+              }
+              x[i][2 * ab] = y.x;
+              x[i][2 * ab + 1] = y.y;
             }
+          }
+          if (p.softcap > 0.f) {
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+              for (int t = 0; t < 4; ++t) x[i][t] = p.softcap * kLog2e * tanh_abs(x[i][t]);
+          }
           if (p.slopes || edge) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
@@ -434,18 +534,16 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
             }
           }
           // ---- weights
-          uint32_t vcw[NB];
-          {
-            const uint8_t* z = sv + mx_scale_off<D, FMT>(sub * 4 + c, 0);
-            if constexpr (NB == 4) {
-              const uint4 w = *reinterpret_cast<const uint4*>(z);
-              vcw[0] = w.x; vcw[1] = w.y; vcw[2] = w.z; vcw[3] = w.w;
-            } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(z);
-              vcw[0] = w.x; vcw[1] = w.y;
-            }
+          float4 vsc[NW];
+          if constexpr (NARROW) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(sv + mx_scale_off<D, FMT>(quad, gb));
+            vsc[0] = make_float4(scale_f32(w, 0), scale_f32(w, 1), scale_f32(w, 2), scale_f32(w, 3));
+          } else {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              vsc[b] = reinterpret_cast<const float4*>(sm_scale[NARROW ? 0 : warp][1])[quad * NB + b];
           }
-          uint32_t pw[NT][NB][TERMS][2];
+          uint32_t pw[NT][NW][TERMS][2];
           float pr[NT];
           auto weights = [&]() {
             bool over = false;
@@ -459,22 +557,24 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
               over |= fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3])) > m[i] + kScoreSlack;
               float wm = 0.f;
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                float w[4];
-#pragma unroll
-                for (int t = 0; t < 4; ++t) w[t] = e[t] * scale_f32(vcw[b], t) * rs[i][b];
-                if (edge) {
-#pragma unroll
-                  for (int t = 0; t < 4; ++t)
-                    if (hide >> (4 * i + t) & 1) w[t] = 0.f;
+              for (int b = 0; b < NW; ++b) {
+                float2 w[2] = {mul2(make_float2(e[0], e[1]), make_float2(vsc[b].x, vsc[b].y)),
+                               mul2(make_float2(e[2], e[3]), make_float2(vsc[b].z, vsc[b].w))};
+                w[0] = mul2(w[0], make_float2(rs[i][b], rs[i][b]));
+                w[1] = mul2(w[1], make_float2(rs[i][b], rs[i][b]));
+                if (edge) {   // 0 times the infinity that marks a block of NaN
+                  if (hide >> (4 * i) & 1) w[0].x = 0.f;
+                  if (hide >> (4 * i) & 2) w[0].y = 0.f;
+                  if (hide >> (4 * i) & 4) w[1].x = 0.f;
+                  if (hide >> (4 * i) & 8) w[1].y = 0.f;
                 }
-                wm = fmaxf(wm, fmaxf(fmaxf(w[0], w[1]), fmaxf(w[2], w[3])));
+                wm = fmaxf(wm, fmaxf(fmaxf(w[0].x, w[0].y), fmaxf(w[1].x, w[1].y)));
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                  pw[i][b][0][k] = pack_f16(w[2 * k], w[2 * k + 1]);
+                  pw[i][b][0][k] = pack_f16(w[k].x, w[k].y);
                   if constexpr (TERMS == 2) {
                     const float2 hi = unpack_f16(pw[i][b][0][k]);
-                    pw[i][b][1][k] = pack_f16(w[2 * k] - hi.x, w[2 * k + 1] - hi.y);
+                    pw[i][b][1][k] = pack_f16(w[k].x - hi.x, w[k].y - hi.y);
                   }
                 }
               }
@@ -482,34 +582,39 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
             }
             return over;
           };
-          if (__any_sync(0xffffffffu, weights())) {
-            // raise the references to what has been seen, and bring the sums to them
+          // the first tile sets the references, later ones seldom raise them
+          if ((it == 0 && sub == 0) || __any_sync(0xffffffffu, weights())) {
+            {
+              // raise the references to what has been seen, and bring the sums to them
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-              float mx = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3]));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-              const float mn = fmaxf(m[i], mx);
-              if (m[i] != -INFINITY) l[i] *= ex2(m[i] - mn);
-              m[i] = mn;
+              for (int i = 0; i < NT; ++i) {
+                float mx = fmaxf(fmaxf(x[i][0], x[i][1]), fmaxf(x[i][2], x[i][3]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = fmaxf(m[i], mx);
+                if (m[i] != -INFINITY) l[i] *= ex2(m[i] - mn);
+                m[i] = mn;
 #pragma unroll
-              for (int b = 0; b < NB; ++b) {
-                float bm = -INFINITY;
+                for (int b = 0; b < NW; ++b) {
+                  // scales are powers of two: their exponents, 128 for the infinity that marks NaN
+                  const float ve[4] = {vsc[b].x, vsc[b].y, vsc[b].z, vsc[b].w};
+                  float bm = -INFINITY;
 #pragma unroll
-                for (int t = 0; t < 4; ++t) bm = fmaxf(bm, x[i][t] + (float)((int)(vcw[b] >> (8 * t) & 255u) - 127));
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-                const float Mn = fmaxf(M[i][b], bm - kWeightExp);
-                const float fb = M[i][b] == -INFINITY ? 0.f : ex2(M[i][b] - Mn);
-                M[i][b] = Mn;
-                rs[i][b] = Mn == -INFINITY ? 0.f : ex2(mn - Mn);
+                  for (int t = 0; t < 4; ++t) bm = fmaxf(bm, x[i][t] + (float)((int)(__float_as_uint(ve[t]) >> 23) - 127));
+                  bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+                  bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+                  const float Mn = fmaxf(M[i][b], bm - kWeightExp);
+                  const float fb = M[i][b] == -INFINITY ? 0.f : ex2(M[i][b] - Mn);
+                  M[i][b] = Mn;
+                  rs[i][b] = Mn == -INFINITY ? 0.f : ex2(mn - Mn);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float fc = __shfl_sync(0xffffffffu, fb, (2 * c + k) * 4);
+                  for (int k = 0; k < 2; ++k) {
+                    const float fc = __shfl_sync(0xffffffffu, fb, (2 * c + k) * 4);
 #pragma unroll
-                  for (int a = 0; a < 2; ++a) {
-                    o[b][a][i][k] *= fc;
-                    o[b][a][i][2 + k] *= fc;
+                    for (int a = 0; a < 2; ++a) {
+                      o[b][a][i][k] *= fc;
+                      o[b][a][i][2 + k] *= fc;
+                    }
                   }
                 }
               }
@@ -520,41 +625,48 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
           for (int i = 0; i < NT; ++i) l[i] += pr[i];
           // ---- values
 #pragma unroll
-          for (int b = 0; b < NB; b += 2) {
-            uint32_t h[2][4][2];   // [block][channel j][token pair]
-            if constexpr (FMT == LOOPVQ_MX_E4M3) {
+          for (int b = 0; b < NB; b += 2)
+#pragma unroll
+            for (int su = 0; su < SUBS; ++su) {
+              uint32_t hv[2][4][2];   // [block][channel j][token pair]
+              if constexpr (FMT == LOOPVQ_MX_E4M3) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  uint4 w = *reinterpret_cast<const uint4*>(sv + mx_code_off<D, FMT>(sub + su, b + k, lane));
+                  if (edge) {
+                    w.x = drop_nan_codes(w.x);
+                    w.y = drop_nan_codes(w.y);
+                    w.z = drop_nan_codes(w.z);
+                    w.w = drop_nan_codes(w.w);
+                  }
+                  codes_e4m3(w.x, hv[k][0]);
+                  codes_e4m3(w.y, hv[k][1]);
+                  codes_e4m3(w.z, hv[k][2]);
+                  codes_e4m3(w.w, hv[k][3]);
+                }
+              } else {
+                const uint4 w = *reinterpret_cast<const uint4*>(sv + mx_code_off<D, FMT>(sub + su, b, lane));
+                codes_e2m1(w.x, hv[0][0]);
+                codes_e2m1(w.y, hv[0][2]);
+                codes_e2m1(w.z, hv[1][0]);
+                codes_e2m1(w.w, hv[1][2]);
+              }
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                uint4 w = *reinterpret_cast<const uint4*>(sv + mx_code_off<D, FMT>(sub, b + k, lane));
-                if (edge) {
-                  w.x = drop_nan_codes(w.x);
-                  w.y = drop_nan_codes(w.y);
-                  w.z = drop_nan_codes(w.z);
-                  w.w = drop_nan_codes(w.w);
+                const int wb = NARROW ? 0 : b + k;
+                // NARROW: the columns of this block (and half of the tile)
+                const bool mine = !NARROW || (gb == b + k && (SUBS == 1 || half == su));
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                  const uint32_t va[4] = {hv[k][2 * a][0], hv[k][2 * a + 1][0], hv[k][2 * a][1], hv[k][2 * a + 1][1]};
+#pragma unroll
+                  for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < TERMS; ++e)
+                      mma_f16(o[wb][a][i], va, mine ? pw[i][wb][e][0] : 0u, mine ? pw[i][wb][e][1] : 0u, o[wb][a][i]);
                 }
-                codes_e4m3(w.x, h[k][0]);
-                codes_e4m3(w.y, h[k][1]);
-                codes_e4m3(w.z, h[k][2]);
-                codes_e4m3(w.w, h[k][3]);
               }
-            } else {
-              const uint4 w = *reinterpret_cast<const uint4*>(sv + mx_code_off<D, FMT>(sub, b, lane));
-              codes_e2m1(w.x, h[0][0]);
-              codes_e2m1(w.y, h[0][2]);
-              codes_e2m1(w.z, h[1][0]);
-              codes_e2m1(w.w, h[1][2]);
             }
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int a = 0; a < 2; ++a)
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                  for (int e = 0; e < TERMS; ++e)
-                    mma_f16(o[b + k][a][i], h[k][2 * a][0], h[k][2 * a + 1][0], h[k][2 * a][1], h[k][2 * a + 1][1],
-                            pw[i][b + k][e][0], pw[i][b + k][e][1]);
-          }
         }
       }
       __syncwarp();   // every lane has read the slot
@@ -569,45 +681,58 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
 
     // ------------------------------------------------ the unit's rows, or this warp's part of them
     const bool whole = first_tile == 0 && n_tiles == cc.tiles;
-    float* part = p.partials + (size_t)(2 * wid + (first_tile == 0)) * (8 * NT) * (D + 4);
+    float* part = p.partials + (size_t)(2 * wid + (first_tile == 0)) * CHUNK * (D + 4);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      float ls = l[i];
+      float ls = l[i], mt = m[i];
       ls += __shfl_xor_sync(0xffffffffu, ls, 1);
       ls += __shfl_xor_sync(0xffffffffu, ls, 2);
-      const int mine = 8 * i + g;
-      const float lse = ls == 0.f ? -INFINITY : (m[i] + log2f(ls)) * kLn2;
-      if (c == 0 && mine < rows) {
+      const float own = ls;
+      if constexpr (NARROW == 2) {   // the halves: relative to the larger reference
+        const float lo = __shfl_xor_sync(0xffffffffu, ls, 16), mo = __shfl_xor_sync(0xffffffffu, mt, 16);
+        mt = fmaxf(m[i], mo);
+        ls = (m[i] == -INFINITY ? ls : ls * ex2(m[i] - mt)) + (mo == -INFINITY ? lo : lo * ex2(mo - mt));
+      }
+      const int mine = RPG * i + gr;
+      const float lse = ls == 0.f ? -INFINITY : (mt + log2f(ls)) * kLn2;
+      if (c == 0 && gb == 0 && half == 0 && mine < rows) {
         const int rho = rho0 + mine;
         if (!whole) {
-          part[mine * (D + 4) + D] = m[i];
-          part[mine * (D + 4) + D + 1] = ls;
+          *reinterpret_cast<float2*>(part + mine * (D + 4) + D) = make_float2(mt, ls);
         } else if (p.lse) {
           p.lse[(int64_t)(rq.row0 + rho / p.G) * p.Hq + h * p.G + rho % p.G] = lse;
         }
       }
       const float inv = whole ? (ls == 0.f ? 0.f : 1.f / ls) : 1.f;
-      float fb[NB];
+      float fb[NW];   // a row that saw only NaN has no M: its l is NaN
 #pragma unroll
-      for (int b = 0; b < NB; ++b) fb[b] = M[i][b] == -INFINITY ? (ls == 0.f ? 0.f : ls) : ex2(M[i][b] - m[i]) * inv;
+      for (int b = 0; b < NW; ++b) fb[b] = M[i][b] == -INFINITY ? own : ex2(M[i][b] - mt) * inv;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int row = 8 * i + 2 * c + k, rho = rho0 + row;
+        const int col = 2 * c + k;
+        const int row = RPG * i + (NARROW ? col / NB % RPG : col), rho = rho0 + row;
         const int64_t at = ((int64_t)(rq.row0 + rho / p.G) * p.Hq + h * p.G + rho % p.G) * D;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const float fc = __shfl_sync(0xffffffffu, fb[b], (2 * c + k) * 4);
+        for (int b = 0; b < NW; ++b) {
+          const float fc = __shfl_sync(0xffffffffu, fb[b], col * 4);
+          const int ch = 32 * (NARROW ? col % NB : b) + 4 * g;
+          float4 y = make_float4(o[b][0][i][k] * fc, o[b][0][i][2 + k] * fc, o[b][1][i][k] * fc, o[b][1][i][2 + k] * fc);
+          if constexpr (NARROW == 2) {
+            y.x += __shfl_xor_sync(0xffffffffu, y.x, 2);
+            y.y += __shfl_xor_sync(0xffffffffu, y.y, 2);
+            y.z += __shfl_xor_sync(0xffffffffu, y.z, 2);
+            y.w += __shfl_xor_sync(0xffffffffu, y.w, 2);
+            if (c >= 2) continue;
+          }
           if (row >= rows) continue;
-          const float4 y = make_float4(o[b][0][i][k] * fc, o[b][0][i][2 + k] * fc, o[b][1][i][k] * fc,
-                                       o[b][1][i][2 + k] * fc);
           if (!whole) {
-            *reinterpret_cast<float4*>(part + row * (D + 4) + 32 * b + 4 * g) = y;
+            *reinterpret_cast<float4*>(part + row * (D + 4) + ch) = y;
           } else if (p.out_bf16) {
-            const __nv_bfloat162 u0 = __floats2bfloat162_rn(y.x, y.y), u1 = __floats2bfloat162_rn(y.z, y.w);
-            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at + 32 * b + 4 * g) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&u0), *reinterpret_cast<const uint32_t*>(&u1));
+            const __nv_bfloat162 z0 = __floats2bfloat162_rn(y.x, y.y), z1 = __floats2bfloat162_rn(y.z, y.w);
+            *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at + ch) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&z0), *reinterpret_cast<const uint32_t*>(&z1));
           } else {
-            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at + 32 * b + 4 * g) = y;
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) + at + ch) = y;
           }
         }
       }
@@ -617,7 +742,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
       const int rest = cc.tiles - n_tiles;
       p.headers[wid] = make_int4((int)((rest + share - 1) / share), rq.row0, h, rho0 << 8 | rows);
     }
-    if (done < count) mx_next_unit<NT>(p, &cc);
+    if (done < count) mx_next_unit<CHUNK>(p, &cc);
   }
   if (lost) {   // copies that are still on their way end before the block does
     for (int i = done; i < issued; ++i) {
@@ -630,104 +755,151 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT>::kCtas) mx_att
   }
 }
 
-// Adds up a unit's partial results.  Block (w, y) takes the unit that starts
-// in warp w and goes on in warps after it, rows y, y + gridDim.y, ..; each of
-// its warps sums every fourth part relative to the row's largest reference.
-constexpr int kMergeWarps = 4;
-template <int D, int NT>
+// Adds up the partial results of units.  Block (x, y) takes the units that
+// start in the warps of block x of the attention kernel and go on in warps
+// after them, rows y, y + gridDim.y, ..  The references and sums of all parts
+// are in shared memory before the first row is read, so that the rows' loads
+// wait for nothing but memory; eight warps share the parts.
+constexpr int kMergeWarps = 8, kMergeParts = 512;
+template <int D, int CHUNK>
 __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttnParams p) {
   constexpr int kCh = D / 32;   // channels of a lane
   __shared__ float sm_o[kMergeWarps][D];
-  __shared__ float sm_l[kMergeWarps];
+  __shared__ float sm_f[kMergeParts], sm_l[kMergeWarps], sm_m[kMergeWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int w = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int4 hd = __ldcg(p.headers + w);
-  if (hd.x == 0) return;
-  const int rows = hd.w & 255, rho0 = hd.w >> 8;
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
-    auto part = [&](int k) {   // slot 1 of warp w, slot 0 of the next ones
-      return p.partials + ((size_t)(2 * (w + k) + (k == 0)) * (8 * NT) + row) * (D + 4);
-    };
-    float mx = -INFINITY;
-    for (int k = lane; k <= hd.x; k += 32) mx = fmaxf(mx, __ldcg(part(k) + D));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int4 hds[kAttnWarps];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-    const float m0 = mx == -INFINITY ? 0.f : mx;
-    float l = 0.f, o[kCh] = {};
+  for (int i = 0; i < kAttnWarps; ++i) hds[i] = __ldcg(p.headers + blockIdx.x * kAttnWarps + i);
+#pragma unroll 1
+  for (int i = 0; i < kAttnWarps; ++i) {
+    const int4 hd = i == 0 ? hds[0] : i == 1 ? hds[1] : i == 2 ? hds[2] : hds[3];
+    const int w = blockIdx.x * kAttnWarps + i, rows = hd.x ? hd.w & 255 : 0, rho0 = hd.w >> 8;
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+      auto part = [&](int k) {   // slot 1 of warp w, slot 0 of the next ones
+        return p.partials + ((size_t)(2 * (w + k) + (k == 0)) * CHUNK + row) * (D + 4);
+      };
+      float top = -INFINITY, ls = 0.f, o[kCh] = {};
+      for (int k0 = 0; k0 <= hd.x; k0 += kMergeParts) {   // one turn unless there are very many parts
+        const int n = min(kMergeParts, hd.x + 1 - k0);
+        float mk[kMergeParts / (kMergeWarps * 32)], lk[kMergeParts / (kMergeWarps * 32)], mx = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kMergeParts / (kMergeWarps * 32); ++e) {
+          const int k = threadIdx.x + e * kMergeWarps * 32;
+          const float2 v = k < n ? __ldcg(reinterpret_cast<const float2*>(part(k0 + k) + D)) : make_float2(-INFINITY, 0.f);
+          mk[e] = v.x;
+          lk[e] = v.y;
+          mx = fmaxf(mx, v.x);
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        if (lane == 0) sm_m[warp] = mx;
+        __syncthreads();
+        float tn = top;
+#pragma unroll
+        for (int e = 0; e < kMergeWarps; ++e) tn = fmaxf(tn, sm_m[e]);
+        const float m0 = tn == -INFINITY ? 0.f : tn, back = top == -INFINITY ? 0.f : ex2(top - m0);
+        ls *= back;
+#pragma unroll
+        for (int e = 0; e < kCh; ++e) o[e] *= back;
+#pragma unroll
+        for (int e = 0; e < kMergeParts / (kMergeWarps * 32); ++e) {
+          const float f = ex2(mk[e] - m0);
+          sm_f[threadIdx.x + e * kMergeWarps * 32] = f;
+          ls += lk[e] * f;
+        }
+        top = tn;
+        __syncthreads();
 #pragma unroll 4
-    for (int k = warp; k <= hd.x; k += kMergeWarps) {
-      const float* q = part(k);
-      const float f = ex2(__ldcg(q + D) - m0);
-      l += __ldcg(q + D + 1) * f;
-      if constexpr (kCh == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + lane);
-        o[0] = fmaf(v.x, f, o[0]);
-        o[1] = fmaf(v.y, f, o[1]);
-        o[2] = fmaf(v.z, f, o[2]);
-        o[3] = fmaf(v.w, f, o[3]);
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2*>(q) + lane);
-        o[0] = fmaf(v.x, f, o[0]);
-        o[1] = fmaf(v.y, f, o[1]);
+        for (int k = warp; k < n; k += kMergeWarps) {
+          const float f = sm_f[k];
+          const float* q = part(k0 + k);
+          if constexpr (kCh == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + lane);
+            o[0] = fmaf(v.x, f, o[0]);
+            o[1] = fmaf(v.y, f, o[1]);
+            o[2] = fmaf(v.z, f, o[2]);
+            o[3] = fmaf(v.w, f, o[3]);
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(q) + lane);
+            o[0] = fmaf(v.x, f, o[0]);
+            o[1] = fmaf(v.y, f, o[1]);
+          }
+        }
+        __syncthreads();   // the next turn writes sm_f and sm_m
       }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, d);
+      if (lane == 0) sm_l[warp] = ls;
+#pragma unroll
+      for (int e = 0; e < kCh; ++e) sm_o[warp][lane * kCh + e] = o[e];
+      __syncthreads();
+      float l = 0.f;
+#pragma unroll
+      for (int e = 0; e < kMergeWarps; ++e) l += sm_l[e];
+      const int rho = rho0 + row, d = threadIdx.x;
+      const int64_t at = (int64_t)(hd.y + rho / p.G) * p.Hq + hd.z * p.G + rho % p.G;
+      if (d < D) {
+        float y = 0.f;
+#pragma unroll
+        for (int e = 0; e < kMergeWarps; ++e) y += sm_o[e][d];
+        y *= l == 0.f ? 0.f : 1.f / l;
+        if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + d] = __float2bfloat16_rn(y);
+        else reinterpret_cast<float*>(p.out)[at * D + d] = y;
+      }
+      if (d == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+      __syncthreads();
     }
-#pragma unroll
-    for (int i = 0; i < kCh; ++i) sm_o[warp][lane * kCh + i] = o[i];
-    if (lane == 0) sm_l[warp] = l;
-    __syncthreads();
-    float ls = 0.f;
-#pragma unroll
-    for (int i = 0; i < kMergeWarps; ++i) ls += sm_l[i];
-    const int rho = rho0 + row;
-    const int64_t at = (int64_t)(hd.y + rho / p.G) * p.Hq + hd.z * p.G + rho % p.G;
-    const float inv = ls == 0.f ? 0.f : 1.f / ls;
-    const int d = threadIdx.x;
-    if (d < D) {
-      float y = 0.f;
-#pragma unroll
-      for (int i = 0; i < kMergeWarps; ++i) y += sm_o[i][d];
-      y *= inv;
-      if (p.out_bf16) reinterpret_cast<__nv_bfloat16*>(p.out)[at * D + d] = __float2bfloat16_rn(y);
-      else reinterpret_cast<float*>(p.out)[at * D + d] = y;
-    }
-    if (d == 0 && p.lse) p.lse[at] = ls == 0.f ? -INFINITY : (mx + log2f(ls)) * kLn2;
-    __syncthreads();
   }
 }
 
-// Rows of a chunk: 16 where a request can have more than 8 (the codes are
-// converted once for both halves), else 8.
-int attn_groups(const loopvq_mx_desc* d, const loopvq_mx_layout* l) {
-  return (int64_t)l->max_new * (d->n_heads_q / d->n_heads_kv) > 8 ? 2 : 1;
+// The variant of a call: columns per row, groups.
+struct AttnVariant {
+  int narrow, nt, chunk, ctas;
+};
+template <int D, int FMT>
+AttnVariant attn_variant_t(int64_t rows, bool fine) {
+  AttnVariant v;
+  constexpr int kFew = MxRows<D, 1>::kPerGroup;
+  v.narrow = rows <= kFew / 2 ? 2 : rows <= (fine ? kFew : 2 * kFew);
+  const int per = v.narrow ? kFew / v.narrow : 8;
+  v.nt = rows > per ? 2 : 1;
+  v.chunk = per * v.nt;
+  v.ctas = v.narrow == 2 ? MxRing<D, FMT, 2, 1>::kCtas
+           : v.narrow    ? (v.nt == 2 ? MxRing<D, FMT, 1, 2>::kCtas : MxRing<D, FMT, 1, 1>::kCtas)
+                         : (v.nt == 2 ? MxRing<D, FMT, 0, 2>::kCtas : MxRing<D, FMT, 0, 1>::kCtas);
+  return v;
 }
-int attn_ctas(int D, int fmt) {
-  const int n = device_sm_count();
-  if (D == 128) return n * (fmt == LOOPVQ_MX_E4M3 ? MxRing<128, LOOPVQ_MX_E4M3>::kCtas : MxRing<128, LOOPVQ_MX_E2M1>::kCtas);
-  return n * (fmt == LOOPVQ_MX_E4M3 ? MxRing<64, LOOPVQ_MX_E4M3>::kCtas : MxRing<64, LOOPVQ_MX_E2M1>::kCtas);
-}
-constexpr int kMinTiles = 2;
-// Blocks of the launch: no more than the warps that could get their least share.
-int attn_grid(const loopvq_mx_desc* d, const loopvq_mx_layout* l) {
-  const int nt = attn_groups(d, l);
+AttnVariant attn_variant(const loopvq_mx_desc* d, const loopvq_mx_layout* l, bool fine) {
   const int64_t rows = (int64_t)l->max_new * (d->n_heads_q / d->n_heads_kv);
-  const int64_t chunks = (rows + 8 * nt - 1) / (8 * nt), tiles = ((int64_t)l->max_ctx_len + kMxTile - 1) / kMxTile;
-  const int most = attn_ctas(d->head_dim, d->format);
-  const int64_t each = (int64_t)d->n_heads_kv * chunks;   // all products below stay under 2^63: see the checks
+  if (d->head_dim == 128)
+    return d->format == LOOPVQ_MX_E4M3 ? attn_variant_t<128, LOOPVQ_MX_E4M3>(rows, fine)
+                                       : attn_variant_t<128, LOOPVQ_MX_E2M1>(rows, fine);
+  return d->format == LOOPVQ_MX_E4M3 ? attn_variant_t<64, LOOPVQ_MX_E4M3>(rows, fine)
+                                     : attn_variant_t<64, LOOPVQ_MX_E2M1>(rows, fine);
+}
+constexpr int kMinTiles = 1;
+// Blocks of the launch: no more than the warps that could get their least share.
+int attn_grid(const loopvq_mx_desc* d, const loopvq_mx_layout* l, const AttnVariant& v) {
+  const int64_t rows = (int64_t)l->max_new * (d->n_heads_q / d->n_heads_kv);
+  const int64_t chunks = (rows + v.chunk - 1) / v.chunk, tiles = ((int64_t)l->max_ctx_len + kMxTile - 1) / kMxTile;
+  const int most = device_sm_count() * v.ctas;
+  const int64_t each = (int64_t)d->n_heads_kv * chunks;
   const int64_t per_cta = (int64_t)kMinTiles * kAttnWarps;
   if (each * tiles >= most * per_cta) return most;
   const int64_t n = (each * tiles * l->batch + per_cta - 1) / per_cta;
   return n < 1 ? 1 : n < most ? (int)n : most;
 }
 
-template <int D, int FMT, int TERMS, int NT>
-loopvq_status launch_attn(const MxAttnParams& p, int grid, int rows, cudaStream_t s) {
-  constexpr int smem = MxRing<D, FMT>::kBytes;
-  auto kfn = mx_attn_kernel<D, FMT, TERMS, NT>;
+template <int D, int FMT, int NARROW, int TERMS, int NT>
+loopvq_status launch_attn(const MxAttnParams& p, int grid, int64_t rows, cudaStream_t s) {
+  constexpr int smem = MxRing<D, FMT, NARROW, NT>::kBytes, CHUNK = MxRows<D, NARROW>::kPerGroup * NT;
+  auto kfn = mx_attn_kernel<D, FMT, NARROW, TERMS, NT>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LOOPVQ_ERR_CUDA;
   kfn<<<grid, kAttnWarps * 32, smem, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid * kAttnWarps, rows < 8 * NT ? rows : 8 * NT);
+  cfg.gridDim = dim3(grid, (unsigned)(rows < CHUNK ? rows : CHUNK));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -735,7 +907,17 @@ loopvq_status launch_attn(const MxAttnParams& p, int grid, int rows, cudaStream_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, NT>, p) == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, CHUNK>, p) == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+}
+template <int D, int FMT>
+loopvq_status launch_attn_v(const MxAttnParams& p, const AttnVariant& v, bool fine, int grid, int64_t rows,
+                            cudaStream_t s) {
+  if (v.narrow == 2) return fine ? launch_attn<D, FMT, 2, 2, 1>(p, grid, rows, s) : launch_attn<D, FMT, 2, 1, 1>(p, grid, rows, s);
+  if (v.narrow)
+    return fine ? launch_attn<D, FMT, 1, 2, 1>(p, grid, rows, s)
+                : v.nt == 2 ? launch_attn<D, FMT, 1, 1, 2>(p, grid, rows, s) : launch_attn<D, FMT, 1, 1, 1>(p, grid, rows, s);
+  if (fine) return v.nt == 2 ? launch_attn<D, FMT, 0, 2, 2>(p, grid, rows, s) : launch_attn<D, FMT, 0, 2, 1>(p, grid, rows, s);
+  return v.nt == 2 ? launch_attn<D, FMT, 0, 1, 2>(p, grid, rows, s) : launch_attn<D, FMT, 0, 1, 1>(p, grid, rows, s);
 }
 
 loopvq_status attn_checks(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout, MxLayout* L) {
@@ -748,11 +930,11 @@ loopvq_status attn_checks(const loopvq_mx_desc* desc, const loopvq_mx_layout* la
 struct AttnWs {
   size_t partials_off, total;
 };
-AttnWs attn_ws(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout) {
-  const size_t warps = (size_t)attn_grid(desc, layout) * kAttnWarps;
+AttnWs attn_ws(const loopvq_mx_desc* desc, int grid, int chunk) {
+  const size_t warps = (size_t)grid * kAttnWarps;
   AttnWs w;
   w.partials_off = (warps * sizeof(int4) + 255) & ~(size_t)255;
-  w.total = w.partials_off + warps * 2 * 8 * attn_groups(desc, layout) * (desc->head_dim + 4) * sizeof(float);
+  w.total = w.partials_off + warps * 2 * chunk * (desc->head_dim + 4) * sizeof(float);
   return w;
 }
 
@@ -764,7 +946,13 @@ using namespace loopvq;
 extern "C" size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout) {
   MxLayout L;
   if (attn_checks(desc, layout, &L) != LOOPVQ_OK) return 0;
-  return attn_ws(desc, layout).total;
+  size_t most = 0;   // of both precisions
+  for (int fine = 0; fine < 2; ++fine) {
+    const AttnVariant v = attn_variant(desc, layout, fine);
+    const size_t n = attn_ws(desc, attn_grid(desc, layout, v), v.chunk).total;
+    if (n > most) most = n;
+  }
+  return most;
 }
 
 extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
@@ -789,7 +977,11 @@ extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq
   const uintptr_t qs = q_dtype == LOOPVQ_BF16 ? 2 : 4;
   if (!q || (uintptr_t)q % qs || !out || ((uintptr_t)out & 15)) return LOOPVQ_ERR_INVALID_ARG;
   if (!workspace || ((uintptr_t)workspace & 255)) return LOOPVQ_ERR_INVALID_ARG;
-  const AttnWs ws = attn_ws(desc, layout);
+  // two fp16 terms of q and of the weights
+  const bool fine = q_dtype == LOOPVQ_F32 || out_dtype == LOOPVQ_F32;
+  const AttnVariant v = attn_variant(desc, layout, fine);
+  const int grid = attn_grid(desc, layout, v);
+  const AttnWs ws = attn_ws(desc, grid, v.chunk);
   if (workspace_bytes < ws.total) return LOOPVQ_ERR_WORKSPACE_TOO_SMALL;
   const size_t step = (size_t)desc->n_heads_kv * p.L.pool_tiles * mx_tile_bytes(desc->head_dim, desc->format);
   p.H = desc->n_heads_kv;
@@ -813,14 +1005,11 @@ extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq
   p.partials = (float*)((uint8_t*)workspace + ws.partials_off);
   p.min_tiles = kMinTiles;
   p.fault = fault_bits;
-  const int grid = attn_grid(desc, layout), nt = attn_groups(desc, layout);
-  const int rows = (int)((int64_t)layout->max_new * p.G < 16 ? layout->max_new * p.G : 16);
-  const bool fine = q_dtype == LOOPVQ_F32 || out_dtype == LOOPVQ_F32;   // two fp16 terms of q and of the weights
+  const int64_t rows = (int64_t)layout->max_new * p.G;
   cudaStream_t s = (cudaStream_t)stream;
-#define MX_ATTN_NT(D_, F_)                                                                                        \
-  (fine ? (nt == 2 ? launch_attn<D_, F_, 2, 2>(p, grid, rows, s) : launch_attn<D_, F_, 2, 1>(p, grid, rows, s))   \
-        : (nt == 2 ? launch_attn<D_, F_, 1, 2>(p, grid, rows, s) : launch_attn<D_, F_, 1, 1>(p, grid, rows, s)))
   if (desc->head_dim == 128)
-    return desc->format == LOOPVQ_MX_E4M3 ? MX_ATTN_NT(128, LOOPVQ_MX_E4M3) : MX_ATTN_NT(128, LOOPVQ_MX_E2M1);
-  return desc->format == LOOPVQ_MX_E4M3 ? MX_ATTN_NT(64, LOOPVQ_MX_E4M3) : MX_ATTN_NT(64, LOOPVQ_MX_E2M1);
+    return desc->format == LOOPVQ_MX_E4M3 ? launch_attn_v<128, LOOPVQ_MX_E4M3>(p, v, fine, grid, rows, s)
+                                          : launch_attn_v<128, LOOPVQ_MX_E2M1>(p, v, fine, grid, rows, s);
+  return desc->format == LOOPVQ_MX_E4M3 ? launch_attn_v<64, LOOPVQ_MX_E4M3>(p, v, fine, grid, rows, s)
+                                        : launch_attn_v<64, LOOPVQ_MX_E2M1>(p, v, fine, grid, rows, s);
 }

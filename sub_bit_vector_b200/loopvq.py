@@ -403,11 +403,16 @@ def _mx_rows(desc, layout, first_step, n_steps, a, b, stride_t, stride_n, stride
 def _prepared(name, args, keep, stream):
     """A zero-argument call of entry point ``name``; without a stream, on
     torch's current one at the time of each call."""
+    import torch
     fn = getattr(_lib, name)
+    plain = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t)
+    args = tuple(t(a) if t in plain else a for t, a in zip(fn.argtypes, args))     # converted once
+    # the current stream of the buffers' device: a tenth of the cost of torch.cuda.current_stream()
+    current, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device()
     at = None if stream is None else _stream(stream)
 
     def call():
-        st = fn(*args, _stream(None) if at is None else at)
+        st = fn(*args, current(device) if at is None else at)
         if st != LOOPVQ_OK:
             raise LoopVQError(name, st)
     call._keep = keep

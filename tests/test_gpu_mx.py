@@ -97,13 +97,14 @@ def _values(rng, shape, kind, bf16=False):
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("order", ["packed", "fused", "odd"])
-def test_write_and_read_bytes(fmt, D, dtype, order):
+@pytest.mark.parametrize("new", [[5, 0, 1, 100, 64], [5, 0, 1, 16, 3], [1, 1, 0, 1, 1]])
+def test_write_and_read_bytes(fmt, D, dtype, order, new):
     """New tokens of ragged requests (none, one, a partial quad, a whole page and
     more) at odd starts: their bytes are the oracle's, all others keep theirs,
     and reading gives the codes' values.  Inputs packed, in a fused
     projection, or at an odd address (scalar loads)."""
     T, H = 2, 3
-    s = Setup([37, 70, 5, 129, 64], [5, 0, 1, 100, 64], D=D, fmt=fmt, T=T, H=H, page=32, seed=D + len(order), fill=0xA5)
+    s = Setup([37, 70, 5, 129, 64], new, D=D, fmt=fmt, T=T, H=H, page=32, seed=D + len(order), fill=0xA5)
     K = _values(s.rng, (T, s.rows, H, D), "k", dtype == "bf16")
     V = _values(s.rng, (T, s.rows, H, D), "v", dtype == "bf16")
     if order == "fused":
