@@ -32,17 +32,22 @@
 namespace loopvq {
 namespace {
 
-constexpr int kAttnWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kIdleLimit = 1u << 23;   // polls of the feeding warp, a third of a second at least
 constexpr float kScoreSlack = 10.f, kWeightMax = 32768.f, kWeightExp = 8.f;
 
+// One block per SM: kWarps warps that compute and one that feeds them.  Each
+// has a ring of kStages slots (a tile of K and its tile of V); 100 to 200 KB per
+// SM are on their way at a time.  With the feeding warp that is 16 warps of up to
+// 128 registers, 12 of 168, or 8 of 255.
 template <int D, int FMT, int NARROW, int NT>
 struct MxRing {
-  static constexpr int kSlot = 2 * MxTile<D, FMT>::kBytes;   // K tile, V tile
-  static constexpr int kStages = kSlot > 8000 ? 2 : 3;
-  static constexpr int kBytes = kAttnWarps * kStages * kSlot;
-  static constexpr int kMost = NARROW ? 4 : (D == 128 ? 4 : 5) - NT;   // by registers
-  static constexpr int kCtas = 216 * 1024 / kBytes < kMost ? 216 * 1024 / kBytes : kMost;   // per SM
+  static constexpr int kSlot = 2 * MxTile<D, FMT>::kBytes;
+  static constexpr int kWarps = NARROW ? (kSlot > 8000 ? 11 : 15) : NT == 1 ? 11 : 7;
+  static constexpr int kFit = 212 * 1024 / (kWarps * kSlot);
+  static constexpr int kStages = kFit < 4 ? kFit : 4;
+  static constexpr int kBytes = kWarps * kStages * kSlot;
+  static_assert(kStages >= 2, "one slot is read while the next arrives");
 };
 
 struct MxAttnParams {
@@ -58,9 +63,9 @@ struct MxAttnParams {
   void* out;
   int out_bf16;
   float* lse;
+  int n_warps;
   int4* headers;     // per warp: the unit that starts in it and goes on
   float* partials;   // per warp: 2 slots (a unit that began earlier; one that goes on) of [chunk][D + 4]
-  int min_tiles;     // least tiles of a warp
   uint32_t* fault;
 };
 
@@ -74,6 +79,23 @@ __device__ __forceinline__ float tanh_abs(float y) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(2.f * kLog2e * y)));
   return fmaf(-2.f, r, 1.f);
+}
+// 8 channels of a query row.
+template <typename T>
+__device__ __forceinline__ void load_query(const void* q, int64_t at, int vec, float* v) {
+  const T* x = reinterpret_cast<const T*>(q) + at;
+  if (!vec) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = to_f32<T>(x[k]);
+    return;
+  }
+  __align__(16) uint32_t w[sizeof(T) * 2];
+#pragma unroll
+  for (int k = 0; k < (int)sizeof(T) / 2; ++k)
+    reinterpret_cast<uint4*>(w)[k] = __ldg(reinterpret_cast<const uint4*>(x) + k);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    v[k] = sizeof(T) == 4 ? __uint_as_float(w[k % (sizeof(T) * 2)]) : k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
 }
 // d = a (16 x 16) b (16 x 8) + c
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
@@ -213,93 +235,113 @@ __device__ __forceinline__ void mx_next_unit(const MxAttnParams& p, MxCursor* c)
 }
 
 template <int D, int FMT, int NARROW, int TERMS, int NT>
-__global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::kCtas) mx_attn_kernel(const MxAttnParams p) {
+__global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32, 1) mx_attn_kernel(const MxAttnParams p) {
   using Tile = MxTile<D, FMT>;
   using Ring = MxRing<D, FMT, NARROW, NT>;
-  constexpr int NB = Tile::kBlocks, S = Ring::kStages;
+  constexpr int NB = Tile::kBlocks, S = Ring::kStages, W = Ring::kWarps;
   constexpr int RPG = MxRows<D, NARROW>::kPerGroup, CHUNK = RPG * NT;
   constexpr int MT = TERMS == 2 ? NT : (NT + 1) / 2;   // 16-row operands of the score product
   constexpr bool kBoth = TERMS == 2 || NT > 1;         // both halves of the 16 rows are used
   constexpr int NW = NARROW ? 1 : NB;                  // blocks that a lane weighs
   extern __shared__ __align__(128) uint8_t sm_ring[];
-  __shared__ __align__(8) uint64_t bars[kAttnWarps][S];
-  __shared__ __align__(16) float sm_scale[NARROW ? 1 : kAttnWarps][2][NARROW ? 4 : 32 * NB];   // of the tile: K, V
+  __shared__ __align__(8) uint64_t full[W][S], empty[W][S];
+  __shared__ __align__(16) float sm_scale[NARROW ? 1 : W][2][NARROW ? 4 : 32 * NB];   // of the tile: K, V
+  __shared__ MxCursor sm_start[W];
+  __shared__ int sm_count[W];
+  __shared__ uint32_t sm_bad[W];   // bit per slot: its tile's page is not in the pool
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   constexpr int SUBS = NARROW == 2 ? 2 : 1;            // halves of a tile that are in flight together
   const int gb = NARROW ? g % NB : 0;                  // this lane's block,
   const int gr = NARROW ? g / NB % RPG : g;            // row in a group,
   const int half = NARROW == 2 ? g >> 2 : 0;           // half of the tile (NARROW 2)
-  const int n_warps = gridDim.x * kAttnWarps, wid = blockIdx.x * kAttnWarps + warp;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int n_warps = p.n_warps, wid = blockIdx.x * W + warp;
 
-  // this warp's share of the list
-  int u0 = 0, t0 = 0;
-  if (lane < p.L.batch) u0 = mx_units<CHUNK>(p, lane, &t0);
-  int64_t total = (int64_t)u0 * t0;
-  for (int r = lane + 32; r < p.L.batch; r += 32) {
-    int tiles;
-    const int units = mx_units<CHUNK>(p, r, &tiles);
-    total += (int64_t)units * tiles;
-  }
+  // each warp's share of the list: `extra` warps take one tile more than the others
+  int64_t share = 0, begin = 0;
+  int extra = 0, count = 0;
+  MxCursor cc = {};
+  if (warp < W) {
+    int u0 = 0, t0 = 0;
+    if (lane < p.L.batch) u0 = mx_units<CHUNK>(p, lane, &t0);
+    int64_t total = (int64_t)u0 * t0;
+    for (int r = lane + 32; r < p.L.batch; r += 32) {
+      int tiles;
+      const int units = mx_units<CHUNK>(p, r, &tiles);
+      total += (int64_t)units * tiles;
+    }
 #pragma unroll
-  for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-  int64_t share = (total + n_warps - 1) / n_warps;
-  if (share < p.min_tiles) share = p.min_tiles;
-  const int64_t begin = wid * share;
-  const int64_t left = total - begin;
-  const int count = left <= 0 ? 0 : (int)(left < share ? left : share);
-  if (lane == 0) p.headers[wid] = make_int4(0, 0, 0, 0);
-  if (count == 0) return;
-
-  if (lane == 0) {
-    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
-  uint8_t* ring = sm_ring + warp * S * Ring::kSlot;
-
-  MxCursor cc = mx_seek<CHUNK>(p, begin, u0, t0, lane);   // consumer
-  MxCursor pc = cc;                                       // producer
-  const int per = p.L.page_tokens / kMxTile;
-  int page = pc.t / per, in_page = pc.t % per, issued = 0;
-  uint32_t bad = 0;   // bit per slot: its tile's page is not in the pool
-  int id = 0;         // the page of the producer's tile
-  int64_t head = 0;   // first tile of its head
-  auto enter_unit = [&]() { head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles; };
-  auto enter_page = [&]() { id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page); };
-  enter_unit();
-  enter_page();
-  auto issue = [&](int slot) {
-    const bool ok = id >= 0 && id < p.L.n_pages;
-    bad = (bad & ~(1u << slot)) | (ok ? 0u : 1u << slot);
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    share = total / n_warps;
+    extra = (int)(total % n_warps);
+    begin = wid * share + min(wid, extra);
+    count = (int)share + (wid < extra);
+    if (count) cc = mx_seek<CHUNK>(p, begin, u0, t0, lane);
     if (lane == 0) {
-      const uint32_t bar = smem_u32(&bars[warp][slot]);
-      if (ok) {
+      p.headers[wid] = make_int4(0, 0, 0, 0);
+      sm_start[warp] = cc;
+      sm_count[warp] = count;
+      sm_bad[warp] = 0;
+      for (int i = 0; i < S; ++i) {
+        mbar_init(smem_u32(&full[warp][i]), 1);
+        mbar_init(smem_u32(&empty[warp][i]), 1);
+      }
+      fence_mbar_init();
+    }
+  }
+  __syncthreads();
+
+  if (warp == W) {   // the feeding warp: lane w fills the ring of warp w
+    const int n = lane < W ? sm_count[lane] : 0;
+    if (n == 0) return;
+    MxCursor pc = sm_start[lane];
+    const int per = p.L.page_tokens / kMxTile;
+    int page = pc.t / per, in_page = pc.t % per, slot = 0;
+    uint32_t phase = 1, idle = 0;   // a wait for the phase before the first does not block
+    int64_t head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
+    int id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+    const uint32_t ring = smem_u32(sm_ring) + lane * S * Ring::kSlot;
+    for (int i = 0; i < n;) {
+      if (!mbar_test(smem_u32(&empty[lane][slot]), phase)) {
+        if (++idle > kIdleLimit) {   // the warp has given up: nothing of this ring is read any more
+          set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
+          return;
+        }
+        __nanosleep(40);
+        continue;
+      }
+      idle = 0;
+      const uint32_t bar = smem_u32(&full[lane][slot]);
+      if (id >= 0 && id < p.L.n_pages) {
         const int64_t at = (head + (int64_t)id * per + in_page) * Tile::kBytes;
-        const uint32_t dst = smem_u32(ring + slot * Ring::kSlot);
         mbar_arrive_expect_tx(bar, 2 * Tile::kBytes);
-        bulk_g2s(dst, p.pk + at, Tile::kBytes, bar);
-        bulk_g2s(dst + Tile::kBytes, p.pv + at, Tile::kBytes, bar);
+        bulk_g2s(ring + slot * Ring::kSlot, p.pk + at, Tile::kBytes, bar);
+        bulk_g2s(ring + slot * Ring::kSlot + Tile::kBytes, p.pv + at, Tile::kBytes, bar);
       } else {
         set_fault(p.fault, LOOPVQ_FAULT_POOL_RANGE);
+        atomicOr(&sm_bad[lane], 1u << slot);   // before the arrival that publishes it
         mbar_arrive(bar);
       }
-    }
-    if (++issued < count) {
+      if (++slot == S) {
+        slot = 0;
+        phase ^= 1;
+      }
+      if (++i == n) break;
       if (++pc.t == pc.tiles) {
         mx_next_unit<CHUNK>(p, &pc);
         page = in_page = 0;
-        enter_unit();
-        enter_page();
+        head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
+        id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages);
       } else if (++in_page == per) {
         in_page = 0;
         ++page;
-        enter_page();
+        id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
       }
     }
-  };
-  for (int i = 0; i < S && i < count; ++i) issue(i);
+    return;
+  }
 
+  const uint8_t* const ring = sm_ring + warp * S * Ring::kSlot;
   int done = 0, slot = 0;
   uint32_t phase = 0;
   bool lost = false;
@@ -312,47 +354,40 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::k
     const int first_tile = cc.t, n_tiles = min(cc.tiles - cc.t, count - done);
     const uint64_t all_new = rq.n >= 64 ? ~0ull : (1ull << rq.n) - 1;
 
-    // query rows: scaled by a power of two (NARROW: of each block) to a largest
-    // magnitude in [2^14, 2^15), as fp16 (TERMS = 2: and the rest)
-    uint32_t qa[MT][NB][2][4] = {};
+    // query rows
+    float v[NT][NW][8] = {};
     float f[NT], slope[NT];
     uint64_t sees[NT];
     int pos_q[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int rho = rho0 + RPG * i + gr;
-      f[i] = slope[i] = 0.f;
+      slope[i] = 0.f;
       sees[i] = 0;
       pos_q[i] = 0;
-      float v[NW][8] = {};
-      float mx = 0.f;
       if (rho < rq.n * p.G) {
         const int node = rho / p.G, hq = h * p.G + rho % p.G;
         const int64_t at = (int64_t)(rq.row0 + node) * p.qn + (int64_t)hq * p.qh + 32 * gb + 8 * c;
 #pragma unroll
         for (int b = 0; b < NW; ++b) {
-          if (p.q_bf16) {
-            const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(p.q) + at + 32 * b;
-            if (p.q_vec) {
-              const uint4 w = __ldg(reinterpret_cast<const uint4*>(x));
-              v[b][0] = bf16_lo(w.x); v[b][1] = bf16_hi(w.x); v[b][2] = bf16_lo(w.y); v[b][3] = bf16_hi(w.y);
-              v[b][4] = bf16_lo(w.z); v[b][5] = bf16_hi(w.z); v[b][6] = bf16_lo(w.w); v[b][7] = bf16_hi(w.w);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) v[b][k] = __bfloat162float(x[k]);
-            }
-          } else {
-            const float* x = reinterpret_cast<const float*>(p.q) + at + 32 * b;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[b][k] = __ldg(x + k);
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(v[b][k]));
+          if (p.q_bf16) load_query<__nv_bfloat16>(p.q, at + 32 * b, p.q_vec, v[i][b]);
+          else load_query<float>(p.q, at + 32 * b, p.q_vec, v[i][b]);
         }
         sees[i] = (p.tree_mask ? __ldg(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
         pos_q[i] = rq.base + __popcll(sees[i] & ~(1ull << node));
         if (p.slopes) slope[i] = __ldg(p.slopes + hq) * kLog2e;
       }
+    }
+    // scaled by a power of two (NARROW: of each block) to a largest magnitude in
+    // [2^14, 2^15), as fp16 (TERMS = 2: and the rest)
+    uint32_t qa[MT][NB][2][4] = {};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      float mx = 0.f;
+#pragma unroll
+      for (int b = 0; b < NW; ++b)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mx = fmaxf(mx, fabsf(v[i][b][k]));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const int ex = max((int)(__float_as_uint(mx) >> 23), 1) - 127;
@@ -365,7 +400,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::k
         for (int k = 0; k < 4; ++k) {
           const int vb = NARROW ? 0 : b;
           const bool has = !NARROW || gb == b;   // NARROW: a row of block b is 0 elsewhere
-          const float x0 = v[vb][2 * k] * up, x1 = v[vb][2 * k + 1] * up;
+          const float x0 = v[i][vb][2 * k] * up, x1 = v[i][vb][2 * k + 1] * up;
           const uint32_t hi = pack_f16(x0, x1);
           // pair k: channels 8c + 2k, 8c + 2k + 1: product k/2, upper half of its 16 channels if k is odd
           if constexpr (TERMS == 1) {
@@ -393,7 +428,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::k
     }
 
     for (int it = 0; it < n_tiles; ++it) {
-      const bool got = mbar_wait_bounded(smem_u32(&bars[warp][slot]), phase);
+      const bool got = mbar_wait_bounded(smem_u32(&full[warp][slot]), phase);
       if (!__all_sync(0xffffffffu, got)) {
         if (lane == 0) set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
         lost = true;
@@ -403,6 +438,7 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::k
       const uint8_t* sv = sk + Tile::kBytes;
       const int tok0 = (first_tile + it) * kMxTile;
       const bool edge = tok0 + kMxTile > rq.base;
+      const uint32_t bad = *reinterpret_cast<volatile uint32_t*>(&sm_bad[warp]);
       if (!(bad >> slot & 1)) {
         if constexpr (!NARROW) {   // the tile's scales as fp32, once for all rows
           if (lane < 8 * NB) {
@@ -670,7 +706,10 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::k
         }
       }
       __syncwarp();   // every lane has read the slot
-      if (issued < count) issue(slot);
+      if (lane == 0) {
+        if (bad >> slot & 1) atomicAnd(&sm_bad[warp], ~(1u << slot));
+        mbar_arrive(smem_u32(&empty[warp][slot]));
+      }
       ++done;
       if (++slot == S) {
         slot = 0;
@@ -739,14 +778,15 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::k
     }
     if (first_tile == 0 && !whole && lane == 0) {
       // the warps after this one that hold the unit's other tiles
-      const int rest = cc.tiles - n_tiles;
-      p.headers[wid] = make_int4((int)((rest + share - 1) / share), rq.row0, h, rho0 << 8 | rows);
+      const int64_t last = begin + done - n_tiles + cc.tiles - 1, longer = (int64_t)extra * (share + 1);
+      const int64_t owner = last < longer ? last / (share + 1) : extra + (last - longer) / share;
+      p.headers[wid] = make_int4((int)(owner - wid), rq.row0, h, rho0 << 8 | rows);
     }
     if (done < count) mx_next_unit<CHUNK>(p, &cc);
   }
   if (lost) {   // copies that are still on their way end before the block does
-    for (int i = done; i < issued; ++i) {
-      mbar_wait_bounded(smem_u32(&bars[warp][slot]), phase);
+    for (int i = 0; i < S; ++i) {
+      mbar_wait_bounded(smem_u32(&full[warp][slot]), phase);
       if (++slot == S) {
         slot = 0;
         phase ^= 1;
@@ -756,11 +796,11 @@ __global__ void __launch_bounds__(kAttnWarps * 32, MxRing<D, FMT, NARROW, NT>::k
 }
 
 // Adds up the partial results of units.  Block (x, y) takes the units that
-// start in the warps of block x of the attention kernel and go on in warps
-// after them, rows y, y + gridDim.y, ..  The references and sums of all parts
+// start in warps 4 x .. 4 x + 3 of the attention kernel and go on in warps after
+// them, rows y, y + gridDim.y, ..  The references and sums of all parts
 // are in shared memory before the first row is read, so that the rows' loads
 // wait for nothing but memory; eight warps share the parts.
-constexpr int kMergeWarps = 8, kMergeParts = 512;
+constexpr int kMergeWarps = 8, kMergeParts = 512, kMergeHeads = 4;
 template <int D, int CHUNK>
 __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttnParams p) {
   constexpr int kCh = D / 32;   // channels of a lane
@@ -768,13 +808,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttn
   __shared__ float sm_f[kMergeParts], sm_l[kMergeWarps], sm_m[kMergeWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int4 hds[kAttnWarps];
+  int4 hds[kMergeHeads];
 #pragma unroll
-  for (int i = 0; i < kAttnWarps; ++i) hds[i] = __ldcg(p.headers + blockIdx.x * kAttnWarps + i);
+  for (int i = 0; i < kMergeHeads; ++i) {
+    const int w = blockIdx.x * kMergeHeads + i;
+    hds[i] = w < p.n_warps ? __ldcg(p.headers + w) : make_int4(0, 0, 0, 0);
+  }
 #pragma unroll 1
-  for (int i = 0; i < kAttnWarps; ++i) {
+  for (int i = 0; i < kMergeHeads; ++i) {
     const int4 hd = i == 0 ? hds[0] : i == 1 ? hds[1] : i == 2 ? hds[2] : hds[3];
-    const int w = blockIdx.x * kAttnWarps + i, rows = hd.x ? hd.w & 255 : 0, rho0 = hd.w >> 8;
+    const int w = blockIdx.x * kMergeHeads + i, rows = hd.x ? hd.w & 255 : 0, rho0 = hd.w >> 8;
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
       auto part = [&](int k) {   // slot 1 of warp w, slot 0 of the next ones
         return p.partials + ((size_t)(2 * (w + k) + (k == 0)) * CHUNK + row) * (D + 4);
@@ -855,7 +898,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttn
 
 // The variant of a call: columns per row, groups.
 struct AttnVariant {
-  int narrow, nt, chunk, ctas;
+  int narrow, nt, chunk, warps;
 };
 template <int D, int FMT>
 AttnVariant attn_variant_t(int64_t rows, bool fine) {
@@ -865,9 +908,9 @@ AttnVariant attn_variant_t(int64_t rows, bool fine) {
   const int per = v.narrow ? kFew / v.narrow : 8;
   v.nt = rows > per ? 2 : 1;
   v.chunk = per * v.nt;
-  v.ctas = v.narrow == 2 ? MxRing<D, FMT, 2, 1>::kCtas
-           : v.narrow    ? (v.nt == 2 ? MxRing<D, FMT, 1, 2>::kCtas : MxRing<D, FMT, 1, 1>::kCtas)
-                         : (v.nt == 2 ? MxRing<D, FMT, 0, 2>::kCtas : MxRing<D, FMT, 0, 1>::kCtas);
+  v.warps = v.narrow == 2 ? MxRing<D, FMT, 2, 1>::kWarps
+           : v.narrow    ? (v.nt == 2 ? MxRing<D, FMT, 1, 2>::kWarps : MxRing<D, FMT, 1, 1>::kWarps)
+                         : (v.nt == 2 ? MxRing<D, FMT, 0, 2>::kWarps : MxRing<D, FMT, 0, 1>::kWarps);
   return v;
 }
 AttnVariant attn_variant(const loopvq_mx_desc* d, const loopvq_mx_layout* l, bool fine) {
@@ -878,28 +921,26 @@ AttnVariant attn_variant(const loopvq_mx_desc* d, const loopvq_mx_layout* l, boo
   return d->format == LOOPVQ_MX_E4M3 ? attn_variant_t<64, LOOPVQ_MX_E4M3>(rows, fine)
                                      : attn_variant_t<64, LOOPVQ_MX_E2M1>(rows, fine);
 }
-constexpr int kMinTiles = 1;
-// Blocks of the launch: no more than the warps that could get their least share.
+// Blocks of the launch: no more than there are warps' worth of tiles.
 int attn_grid(const loopvq_mx_desc* d, const loopvq_mx_layout* l, const AttnVariant& v) {
   const int64_t rows = (int64_t)l->max_new * (d->n_heads_q / d->n_heads_kv);
   const int64_t chunks = (rows + v.chunk - 1) / v.chunk, tiles = ((int64_t)l->max_ctx_len + kMxTile - 1) / kMxTile;
-  const int most = device_sm_count() * v.ctas;
-  const int64_t each = (int64_t)d->n_heads_kv * chunks;
-  const int64_t per_cta = (int64_t)kMinTiles * kAttnWarps;
-  if (each * tiles >= most * per_cta) return most;
-  const int64_t n = (each * tiles * l->batch + per_cta - 1) / per_cta;
+  const int most = device_sm_count();
+  const int64_t each = (int64_t)d->n_heads_kv * chunks * tiles;   // below 2^62
+  if (each >= (int64_t)most * v.warps) return most;
+  const int64_t n = (each * l->batch + v.warps - 1) / v.warps;
   return n < 1 ? 1 : n < most ? (int)n : most;
 }
 
 template <int D, int FMT, int NARROW, int TERMS, int NT>
 loopvq_status launch_attn(const MxAttnParams& p, int grid, int64_t rows, cudaStream_t s) {
-  constexpr int smem = MxRing<D, FMT, NARROW, NT>::kBytes, CHUNK = MxRows<D, NARROW>::kPerGroup * NT;
+  constexpr int smem = MxRing<D, FMT, NARROW, NT>::kBytes, W = MxRing<D, FMT, NARROW, NT>::kWarps, CHUNK = MxRows<D, NARROW>::kPerGroup * NT;
   auto kfn = mx_attn_kernel<D, FMT, NARROW, TERMS, NT>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LOOPVQ_ERR_CUDA;
-  kfn<<<grid, kAttnWarps * 32, smem, s>>>(p);
+  kfn<<<grid, (W + 1) * 32, smem, s>>>(p);
   if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (unsigned)(rows < CHUNK ? rows : CHUNK));
+  cfg.gridDim = dim3((grid * W + kMergeHeads - 1) / kMergeHeads, (unsigned)(rows < CHUNK ? rows : CHUNK));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -930,11 +971,11 @@ loopvq_status attn_checks(const loopvq_mx_desc* desc, const loopvq_mx_layout* la
 struct AttnWs {
   size_t partials_off, total;
 };
-AttnWs attn_ws(const loopvq_mx_desc* desc, int grid, int chunk) {
-  const size_t warps = (size_t)grid * kAttnWarps;
+AttnWs attn_ws(const loopvq_mx_desc* desc, int grid, const AttnVariant& v) {
+  const size_t warps = (size_t)grid * v.warps;
   AttnWs w;
   w.partials_off = (warps * sizeof(int4) + 255) & ~(size_t)255;
-  w.total = w.partials_off + warps * 2 * chunk * (desc->head_dim + 4) * sizeof(float);
+  w.total = w.partials_off + warps * 2 * v.chunk * (desc->head_dim + 4) * sizeof(float);
   return w;
 }
 
@@ -949,7 +990,7 @@ extern "C" size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, con
   size_t most = 0;   // of both precisions
   for (int fine = 0; fine < 2; ++fine) {
     const AttnVariant v = attn_variant(desc, layout, fine);
-    const size_t n = attn_ws(desc, attn_grid(desc, layout, v), v.chunk).total;
+    const size_t n = attn_ws(desc, attn_grid(desc, layout, v), v).total;
     if (n > most) most = n;
   }
   return most;
@@ -981,7 +1022,7 @@ extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq
   const bool fine = q_dtype == LOOPVQ_F32 || out_dtype == LOOPVQ_F32;
   const AttnVariant v = attn_variant(desc, layout, fine);
   const int grid = attn_grid(desc, layout, v);
-  const AttnWs ws = attn_ws(desc, grid, v.chunk);
+  const AttnWs ws = attn_ws(desc, grid, v);
   if (workspace_bytes < ws.total) return LOOPVQ_ERR_WORKSPACE_TOO_SMALL;
   const size_t step = (size_t)desc->n_heads_kv * p.L.pool_tiles * mx_tile_bytes(desc->head_dim, desc->format);
   p.H = desc->n_heads_kv;
@@ -1001,9 +1042,9 @@ extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq
   p.out = out;
   p.out_bf16 = out_dtype == LOOPVQ_BF16;
   p.lse = lse_out;
+  p.n_warps = grid * v.warps;
   p.headers = (int4*)workspace;
   p.partials = (float*)((uint8_t*)workspace + ws.partials_off);
-  p.min_tiles = kMinTiles;
   p.fault = fault_bits;
   const int64_t rows = (int64_t)layout->max_new * p.G;
   cudaStream_t s = (cudaStream_t)stream;
