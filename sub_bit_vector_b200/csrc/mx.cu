@@ -149,7 +149,7 @@ __device__ __forceinline__ bool mx_unit(const MxMoveParams& p, MxUnit* u) {
 // Quantise: K lanes hold 8 channels of two tokens per block, V lanes 4
 // channels of four tokens.
 template <int D, int FMT, typename T, bool VEC>
-__global__ void __launch_bounds__(256) mx_write_kernel(const MxMoveParams p) {
+__global__ void __launch_bounds__(256, 3) mx_write_kernel(const MxMoveParams p) {
   using Tile = MxTile<D, FMT>;
   constexpr int NB = Tile::kBlocks;
   MxUnit u;

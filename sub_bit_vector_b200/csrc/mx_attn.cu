@@ -25,16 +25,12 @@
 // tiles is rare; the sums are rescaled then, and the largest weight stands at
 // 2^8: halfway between fp16's top and where its 11 bits begin to run out, at
 // 2^-22 of the largest weight.
-#include <limits.h>
-
-#include "mx.cuh"
+#include "mx_attn.cuh"
 
 namespace loopvq {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kIdleLimit = 1u << 23;   // polls of the feeding warp, a third of a second at least
-constexpr float kScoreSlack = 10.f, kWeightMax = 32768.f, kWeightExp = 8.f;
 
 // One block per SM: kWarps warps that compute and one that feeds them.  Each
 // has a ring of kStages slots (a tile of K and its tile of V); 100 to 200 KB per
@@ -50,53 +46,6 @@ struct MxRing {
   static_assert(kStages >= 2, "one slot is read while the next arrives");
 };
 
-struct MxAttnParams {
-  MxLayout L;
-  int H, Hq, G;
-  const uint8_t *pk, *pv;   // this loop step's pools
-  const void* q;
-  int q_bf16, q_vec;
-  int64_t qn, qh;
-  const uint64_t* tree_mask;
-  float scale, softcap;
-  const float* slopes;
-  void* out;
-  int out_bf16;
-  float* lse;
-  int n_warps;
-  int4* headers;     // per warp: the unit that starts in it and goes on
-  float* partials;   // per warp: 2 slots (a unit that began earlier; one that goes on) of [chunk][D + 4]
-  uint32_t* fault;
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// tanh y = 1 - 2 / (1 + e^2y), right to 2^-23 absolutely, which is what a score needs.
-__device__ __forceinline__ float tanh_abs(float y) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(2.f * kLog2e * y)));
-  return fmaf(-2.f, r, 1.f);
-}
-// 8 channels of a query row.
-template <typename T>
-__device__ __forceinline__ void load_query(const void* q, int64_t at, int vec, float* v) {
-  const T* x = reinterpret_cast<const T*>(q) + at;
-  if (!vec) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = to_f32<T>(x[k]);
-    return;
-  }
-  __align__(16) uint32_t w[sizeof(T) * 2];
-#pragma unroll
-  for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-    reinterpret_cast<uint4*>(w)[k] = __ldg(reinterpret_cast<const uint4*>(x) + k);
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    v[k] = sizeof(T) == 4 ? __uint_as_float(w[k % (sizeof(T) * 2)]) : k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);
-}
 // d = a (16 x 16) b (16 x 8) + c
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
                                         const float (&c)[4]) {
@@ -106,56 +55,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
-__device__ __forceinline__ uint64_t pair(float2 a) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-  return r;
-}
-__device__ __forceinline__ float2 unpair(uint64_t a) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
-  return r;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)));
-  return unpair(r);
-}
-__device__ __forceinline__ void fma2(float* c, float2 a, float2 b) {   // c[0..1] += a * b
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair(a)), "l"(pair(b)), "l"(pair(make_float2(c[0], c[1]))));
-  const float2 v = unpair(r);
-  c[0] = v.x;
-  c[1] = v.y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ float2 unpack_f16(uint32_t h) { return __half22float2(*reinterpret_cast<__half2*>(&h)); }
-// The 4 codes (e4m3) or 8 (e2m1) of a word as fp16 pairs.
-__device__ __forceinline__ void codes_e4m3(uint32_t w, uint32_t* h) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
-      : "=r"(h[0]), "=r"(h[1])
-      : "r"(w));
-}
-__device__ __forceinline__ void codes_e2m1(uint32_t w, uint32_t* h) {
-  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
-      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-// Scale byte t of a word as 2^e (255: infinity, which codes of 0 turn into NaN).
-__device__ __forceinline__ float scale_f32(uint32_t w, int t) {
-  return __uint_as_float(t == 3 ? (w >> 1) & 0x7f800000u : (w << (23 - 8 * t)) & 0x7f800000u);
-}
-// e4m3 NaN codes to 0.
-__device__ __forceinline__ uint32_t drop_nan_codes(uint32_t w) {
-  const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-  return w & ~((m >> 7) * 0xffu);
-}
-
 // Rows of a request that one warp takes together, as NT groups of columns of
 // the second product.
 //   NARROW 0: a column is a query row; a lane goes through all blocks.
@@ -170,69 +69,6 @@ template <int D, int NARROW>
 struct MxRows {
   static constexpr int kPerGroup = NARROW ? 8 / (D / kMxBlock) / NARROW : 8;
 };
-
-// Where in the list of tiles a warp is.
-struct MxCursor {
-  int r, u, units, t, tiles;   // request, unit of its H * chunks, tile of its ctx
-};
-// Units and tiles of request r (0 units if it has no part in the call).
-template <int CHUNK>
-__device__ __forceinline__ int mx_units(const MxAttnParams& p, int r, int* tiles) {
-  MxReq q;
-  *tiles = 0;
-  if (!mx_request(p.L, r, &q, p.fault) || q.n == 0 || q.n > kMxMaxTree) return 0;
-  *tiles = (q.ctx + kMxTile - 1) / kMxTile;
-  return (q.n * p.G + CHUNK - 1) / CHUNK * p.H;
-}
-// The cursor at tile `at` of the whole list (0 <= at < total); uniform in the
-// warp.  u0, t0: units and tiles of request `lane`.
-template <int CHUNK>
-__device__ __forceinline__ MxCursor mx_seek(const MxAttnParams& p, int64_t at, int u0, int t0, int lane) {
-  MxCursor c = {0, 0, 0, 0, 1};
-  for (int r0 = 0; r0 < p.L.batch; r0 += 32) {
-    int tiles = t0, units = u0;
-    if (r0) {
-      units = tiles = 0;
-      if (r0 + lane < p.L.batch) units = mx_units<CHUNK>(p, r0 + lane, &tiles);
-    }
-    int64_t sum = (int64_t)units * tiles;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, sum, d);
-      if (lane >= d) sum += o;
-    }
-    const int64_t all = __shfl_sync(0xffffffffu, sum, 31);
-    if (at < all) {
-      const int l = __ffs(__ballot_sync(0xffffffffu, at < sum)) - 1;
-      c.r = r0 + l;
-      c.units = __shfl_sync(0xffffffffu, units, l);
-      c.tiles = __shfl_sync(0xffffffffu, tiles, l);
-      const int64_t in = at - (__shfl_sync(0xffffffffu, sum, l) - (int64_t)c.units * c.tiles);
-      c.u = (int)(in / c.tiles);
-      c.t = (int)(in % c.tiles);
-      return c;
-    }
-    at -= all;
-  }
-  return c;
-}
-// On to the next unit; the caller knows that there is one (lengths that
-// change under the kernel are the caller's error; indices stay in range).
-template <int CHUNK>
-__device__ __forceinline__ void mx_next_unit(const MxAttnParams& p, MxCursor* c) {
-  c->t = 0;
-  if (++c->u < c->units) return;
-  c->u = 0;
-  do {
-    if (++c->r >= p.L.batch) {
-      c->r = p.L.batch - 1;
-      c->units = p.H;
-      c->tiles = 1;
-      return;
-    }
-    c->units = mx_units<CHUNK>(p, c->r, &c->tiles);
-  } while (c->units == 0);
-}
 
 template <int D, int FMT, int NARROW, int TERMS, int NT>
 __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32, 1) mx_attn_kernel(const MxAttnParams p) {
@@ -255,7 +91,7 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
   const int gr = NARROW ? g / NB % RPG : g;            // row in a group,
   const int half = NARROW == 2 ? g >> 2 : 0;           // half of the tile (NARROW 2)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int n_warps = p.n_warps, wid = blockIdx.x * W + warp;
+  const int n_warps = p.n_workers, wid = blockIdx.x * W + warp;
 
   // each warp's share of the list: `extra` warps take one tile more than the others
   int64_t share = 0, begin = 0;
@@ -812,7 +648,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttn
 #pragma unroll
   for (int i = 0; i < kMergeHeads; ++i) {
     const int w = blockIdx.x * kMergeHeads + i;
-    hds[i] = w < p.n_warps ? __ldcg(p.headers + w) : make_int4(0, 0, 0, 0);
+    hds[i] = w < p.n_workers ? __ldcg(p.headers + w) : make_int4(0, 0, 0, 0);
   }
 #pragma unroll 1
   for (int i = 0; i < kMergeHeads; ++i) {
@@ -896,9 +732,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttn
   }
 }
 
+constexpr int kRowsFrom = 32;   // more rows than this: mx_rows_kernel
 // The variant of a call: columns per row, groups.
 struct AttnVariant {
-  int narrow, nt, chunk, warps;
+  int narrow, nt, chunk;
+  int workers;   // of the largest launch, and in a block
+  int per_block;
+  bool rows;     // mx_rows_kernel
 };
 template <int D, int FMT>
 AttnVariant attn_variant_t(int64_t rows, bool fine) {
@@ -908,9 +748,16 @@ AttnVariant attn_variant_t(int64_t rows, bool fine) {
   const int per = v.narrow ? kFew / v.narrow : 8;
   v.nt = rows > per ? 2 : 1;
   v.chunk = per * v.nt;
-  v.warps = v.narrow == 2 ? MxRing<D, FMT, 2, 1>::kWarps
+  v.per_block = v.narrow == 2 ? MxRing<D, FMT, 2, 1>::kWarps
            : v.narrow    ? (v.nt == 2 ? MxRing<D, FMT, 1, 2>::kWarps : MxRing<D, FMT, 1, 1>::kWarps)
                          : (v.nt == 2 ? MxRing<D, FMT, 0, 2>::kWarps : MxRing<D, FMT, 0, 1>::kWarps);
+  v.workers = device_sm_count() * v.per_block;
+  v.rows = !fine && rows > kRowsFrom;
+  if (v.rows) {
+    v.chunk = kMxRowsChunk;
+    v.workers = mx_rows_workers();
+    v.per_block = 1;
+  }
   return v;
 }
 AttnVariant attn_variant(const loopvq_mx_desc* d, const loopvq_mx_layout* l, bool fine) {
@@ -925,22 +772,17 @@ AttnVariant attn_variant(const loopvq_mx_desc* d, const loopvq_mx_layout* l, boo
 int attn_grid(const loopvq_mx_desc* d, const loopvq_mx_layout* l, const AttnVariant& v) {
   const int64_t rows = (int64_t)l->max_new * (d->n_heads_q / d->n_heads_kv);
   const int64_t chunks = (rows + v.chunk - 1) / v.chunk, tiles = ((int64_t)l->max_ctx_len + kMxTile - 1) / kMxTile;
-  const int most = device_sm_count();
+  const int most = v.workers / v.per_block;
   const int64_t each = (int64_t)d->n_heads_kv * chunks * tiles;   // below 2^62
-  if (each >= (int64_t)most * v.warps) return most;
-  const int64_t n = (each * l->batch + v.warps - 1) / v.warps;
+  if (each >= v.workers) return most;
+  const int64_t n = (each * l->batch + v.per_block - 1) / v.per_block;
   return n < 1 ? 1 : n < most ? (int)n : most;
 }
 
-template <int D, int FMT, int NARROW, int TERMS, int NT>
-loopvq_status launch_attn(const MxAttnParams& p, int grid, int64_t rows, cudaStream_t s) {
-  constexpr int smem = MxRing<D, FMT, NARROW, NT>::kBytes, W = MxRing<D, FMT, NARROW, NT>::kWarps, CHUNK = MxRows<D, NARROW>::kPerGroup * NT;
-  auto kfn = mx_attn_kernel<D, FMT, NARROW, TERMS, NT>;
-  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LOOPVQ_ERR_CUDA;
-  kfn<<<grid, (W + 1) * 32, smem, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
+template <int D, int CHUNK>
+loopvq_status launch_merge(const MxAttnParams& p, int64_t rows, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((grid * W + kMergeHeads - 1) / kMergeHeads, (unsigned)(rows < CHUNK ? rows : CHUNK));
+  cfg.gridDim = dim3((p.n_workers + kMergeHeads - 1) / kMergeHeads, (unsigned)(rows < CHUNK ? rows : CHUNK));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -950,9 +792,20 @@ loopvq_status launch_attn(const MxAttnParams& p, int grid, int64_t rows, cudaStr
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, CHUNK>, p) == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }
+template <int D, int FMT, int NARROW, int TERMS, int NT>
+loopvq_status launch_attn(const MxAttnParams& p, int grid, int64_t rows, cudaStream_t s) {
+  constexpr int smem = MxRing<D, FMT, NARROW, NT>::kBytes, W = MxRing<D, FMT, NARROW, NT>::kWarps, CHUNK = MxRows<D, NARROW>::kPerGroup * NT;
+  auto kfn = mx_attn_kernel<D, FMT, NARROW, TERMS, NT>;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  kfn<<<grid, (W + 1) * 32, smem, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  return launch_merge<D, CHUNK>(p, rows, s);
+}
 template <int D, int FMT>
 loopvq_status launch_attn_v(const MxAttnParams& p, const AttnVariant& v, bool fine, int grid, int64_t rows,
                             cudaStream_t s) {
+  if (v.rows)
+    return mx_rows_launch(D, FMT, p, grid, s) == cudaSuccess ? launch_merge<D, kMxRowsChunk>(p, rows, s) : LOOPVQ_ERR_CUDA;
   if (v.narrow == 2) return fine ? launch_attn<D, FMT, 2, 2, 1>(p, grid, rows, s) : launch_attn<D, FMT, 2, 1, 1>(p, grid, rows, s);
   if (v.narrow)
     return fine ? launch_attn<D, FMT, 1, 2, 1>(p, grid, rows, s)
@@ -972,7 +825,7 @@ struct AttnWs {
   size_t partials_off, total;
 };
 AttnWs attn_ws(const loopvq_mx_desc* desc, int grid, const AttnVariant& v) {
-  const size_t warps = (size_t)grid * v.warps;
+  const size_t warps = (size_t)grid * v.per_block;
   AttnWs w;
   w.partials_off = (warps * sizeof(int4) + 255) & ~(size_t)255;
   w.total = w.partials_off + warps * 2 * v.chunk * (desc->head_dim + 4) * sizeof(float);
@@ -1042,7 +895,7 @@ extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq
   p.out = out;
   p.out_bf16 = out_dtype == LOOPVQ_BF16;
   p.lse = lse_out;
-  p.n_warps = grid * v.warps;
+  p.n_workers = grid * v.per_block;
   p.headers = (int4*)workspace;
   p.partials = (float*)((uint8_t*)workspace + ws.partials_off);
   p.fault = fault_bits;
