@@ -635,7 +635,22 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
 // start in warps 4 x .. 4 x + 3 of the attention kernel and go on in warps after
 // them, rows y, y + gridDim.y, ..  The references and sums of all parts
 // are in shared memory before the first row is read, so that the rows' loads
-// wait for nothing but memory; eight warps share the parts.
+// wait for nothing but memory; eight warps share the parts of a row.
+// o += f * part, this lane's channels.
+template <int N>
+__device__ __forceinline__ void add_part(const float* part, int lane, float f, float* o) {
+  if constexpr (N == 4) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(part) + lane);
+    o[0] = fmaf(v.x, f, o[0]);
+    o[1] = fmaf(v.y, f, o[1]);
+    o[2] = fmaf(v.z, f, o[2]);
+    o[3] = fmaf(v.w, f, o[3]);
+  } else {
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(part) + lane);
+    o[0] = fmaf(v.x, f, o[0]);
+    o[1] = fmaf(v.y, f, o[1]);
+  }
+}
 constexpr int kMergeWarps = 8, kMergeParts = 512, kMergeHeads = 4;
 template <int D, int CHUNK>
 __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttnParams p) {
@@ -691,19 +706,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttn
         __syncthreads();
 #pragma unroll 4
         for (int k = warp; k < n; k += kMergeWarps) {
-          const float f = sm_f[k];
-          const float* q = part(k0 + k);
-          if constexpr (kCh == 4) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(q) + lane);
-            o[0] = fmaf(v.x, f, o[0]);
-            o[1] = fmaf(v.y, f, o[1]);
-            o[2] = fmaf(v.z, f, o[2]);
-            o[3] = fmaf(v.w, f, o[3]);
-          } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(q) + lane);
-            o[0] = fmaf(v.x, f, o[0]);
-            o[1] = fmaf(v.y, f, o[1]);
-          }
+          add_part<kCh>(part(k0 + k), lane, sm_f[k], o);
         }
         __syncthreads();   // the next turn writes sm_f and sm_m
       }
@@ -730,6 +733,51 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttn
       __syncthreads();
     }
   }
+}
+
+// The same for chunks of many rows: a warp takes a row, 32 parts at a time.
+template <int D, int CHUNK>
+__global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_rows_kernel(const MxAttnParams p) {
+  constexpr int kCh = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
+  const int w = blockIdx.x;
+  const int4 hd = __ldcg(p.headers + w);
+  if (hd.x == 0 || row >= (hd.w & 255)) return;
+  auto part = [&](int k) { return p.partials + ((size_t)(2 * (w + k) + (k == 0)) * CHUNK + row) * (D + 4); };
+  float top = -INFINITY, l = 0.f, o[kCh] = {};
+  for (int k0 = 0; k0 <= hd.x; k0 += 32) {
+    const float2 ml =
+        k0 + lane <= hd.x ? __ldcg(reinterpret_cast<const float2*>(part(k0 + lane) + D)) : make_float2(-INFINITY, 0.f);
+    float tn = fmaxf(top, ml.x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) tn = fmaxf(tn, __shfl_xor_sync(0xffffffffu, tn, d));
+    const float m0 = tn == -INFINITY ? 0.f : tn, back = top == -INFINITY ? 0.f : ex2(top - m0), fl = ex2(ml.x - m0);
+    l = l * back + ml.y * fl;
+#pragma unroll
+    for (int e = 0; e < kCh; ++e) o[e] *= back;
+    const int n = min(32, hd.x + 1 - k0);
+#pragma unroll 4
+    for (int k = 0; k < n; ++k) add_part<kCh>(part(k0 + k), lane, __shfl_sync(0xffffffffu, fl, k), o);
+    top = tn;
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  const int rho = (hd.w >> 8) + row;
+  const int64_t at = (int64_t)(hd.y + rho / p.G) * p.Hq + hd.z * p.G + rho % p.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kCh; ++e) o[e] *= inv;
+  if (p.out_bf16) {
+#pragma unroll
+    for (int e = 0; e < kCh; e += 2)
+      reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at * D + lane * kCh)[e / 2] =
+          __floats2bfloat162_rn(o[e], o[e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kCh; ++e) reinterpret_cast<float*>(p.out)[at * D + lane * kCh + e] = o[e];
+  }
+  if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
 constexpr int kRowsFrom = 32;   // more rows than this: mx_rows_kernel
@@ -782,7 +830,9 @@ int attn_grid(const loopvq_mx_desc* d, const loopvq_mx_layout* l, const AttnVari
 template <int D, int CHUNK>
 loopvq_status launch_merge(const MxAttnParams& p, int64_t rows, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.n_workers + kMergeHeads - 1) / kMergeHeads, (unsigned)(rows < CHUNK ? rows : CHUNK));
+  const int most = (int)(rows < CHUNK ? rows : CHUNK);
+  cfg.gridDim = CHUNK < 8 ? dim3((p.n_workers + kMergeHeads - 1) / kMergeHeads, most)
+                          : dim3(p.n_workers, (most + kMergeWarps - 1) / kMergeWarps);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -790,7 +840,10 @@ loopvq_status launch_merge(const MxAttnParams& p, int64_t rows, cudaStream_t s) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, CHUNK>, p) == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+  cudaError_t e;
+  if constexpr (CHUNK < 8) e = cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, CHUNK>, p);
+  else e = cudaLaunchKernelEx(&cfg, mx_merge_rows_kernel<D, CHUNK>, p);
+  return e == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }
 template <int D, int FMT, int NARROW, int TERMS, int NT>
 loopvq_status launch_attn(const MxAttnParams& p, int grid, int64_t rows, cudaStream_t s) {

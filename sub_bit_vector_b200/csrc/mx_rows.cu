@@ -6,12 +6,14 @@
 // a chunk is 128 rows = the 128 lanes of the accumulators, one thread per row,
 // so that a row's softmax needs no exchange.  Per tile of 32 tokens:
 //   K' (fp16, shared memory) = code * 2^(e - E), E the token's largest scale
-//     exponent; S[128 x 32] = Q K'^T (TMEM), x = S 2^E * scale in fp32.  Exact as
-//     long as a code times 2^(e - E) is an fp16 number; below, a key's element is
-//     rounded to 2^-24 of 2^E.
-//   P_b (fp16, TMEM) = 2^(x + e_b - M_b) for each block b of 32 channels, M_b a
-//     reference per row and block, raised as in mx_attn.cu; O_b[128 x 32] +=
-//     P_b V_b with V's codes as they are (fp16, shared memory).
+//     exponent; S[128 x 32] = Q K'^T (TMEM), x = S 2^E * scale in fp32.
+//   P (fp16, TMEM) = 2^(x + E - M), E the largest exponent of the token's value,
+//     M a reference per row, raised as in mx_attn.cu; V' = code * 2^(e - E);
+//     O[128 x D] += P V'.
+// K' and V' are exact as long as a code times 2^(e - E) is an fp16 number; below,
+// an element is rounded to 2^-24 of 2^E, which is less than 2^-26 of its token's
+// largest element.  A block of NaN counts as 0 in V' and is put into the outputs
+// of the rows that see it at the end.
 // All threads convert K' while the previous tile's P V runs, and V while the
 // scores are computed; two blocks per SM fill each other's waits.
 //
@@ -36,30 +38,32 @@ struct Rows {
   static constexpr int kVLbo = 144, kVSbo = 672, kVBlock = 4 * kVSbo;    // channels x tokens, per block
   static constexpr int kQ = 0, kK = kQ + kMxRowsChunk / 8 * kQSbo, kV = kK + kMxTile / 8 * kKSbo,
                        kRing = kV + NB * kVBlock, kSlot = 2 * Tile::kBytes, kFac = kRing + kStages * kSlot,
-                       kVs = kFac + kMxTile * 4, kVmax = kVs + NB * kMxTile * 4, kPos = kVmax + 16, kBars = kPos + kMxTile * 4,
+                       kVs = kFac + kMxTile * 4, kNan = kVs + kMxTile * 4, kVmax = kNan + 16, kPos = kVmax + 16, kBars = kPos + kMxTile * 4,
                        kNeed = kBars + (kStages + 2) * 8 + 16;
   static constexpr int kBytes = kNeed > 76 * 1024 ? kNeed : 76 * 1024;   // two blocks per SM, no third that would wait for TMEM
   // TMEM columns: O, S, P
   static constexpr int kO = 0, kS = D, kP = D + kMxTile, kCols = D == 128 ? 256 : 128;
-  static_assert(kP + NB * 16 <= kCols, "TMEM");
+  static_assert(kP + 16 <= kCols, "TMEM");
 };
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
   return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)((lbo >> 4) & 0x3FFF) << 16 | (uint64_t)((sbo >> 4) & 0x3FFF) << 32 |
          (uint64_t)1 << 46;   // descriptor version; no swizzle
 }
-// kind::f16, fp16 operands, K-major, fp32 sums, M = 128, N = 32
-constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kMxTile >> 3) << 17) | ((uint32_t)(kMxRowsChunk >> 4) << 24);
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+// kind::f16, fp16 operands, K-major, fp32 sums, M = 128
+constexpr uint32_t idesc(int n) {
+  return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kMxRowsChunk >> 4) << 24);
+}
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(kIdesc), "r"(acc)
+      "l"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t acc) {   // A in TMEM
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {   // A in TMEM
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(kIdesc), "r"(acc)
+      "r"(a), "l"(b), "r"(id), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void umma_commit(uint32_t bar) {
@@ -109,10 +113,9 @@ __device__ __forceinline__ uint32_t mul_f16(uint32_t a, uint32_t s) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(s));
   return r;
 }
-// 2^-d as a pair of fp16 (0 below the least subnormal), d >= 0.
-__device__ __forceinline__ uint32_t pow2_f16x2(int d) {
-  const uint32_t h = d <= 14 ? (uint32_t)(15 - d) << 10 : d <= 24 ? 1u << (24 - d) : 0u;
-  return h | h << 16;
+// 2^(e - E) as fp32 from 2^e and 2^E, 0 where it would be below 2^-126.
+__device__ __forceinline__ float ratio(float e, float E) {
+  return __int_as_float(max(__float_as_int(e) - __float_as_int(E) + 0x3f800000, 0));
 }
 
 template <int D, int FMT>
@@ -126,8 +129,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
   uint64_t* const bar_o = bar_s + 1;  // P V done
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bar_o + 1);
   float* const fac = reinterpret_cast<float*>(sm + R::kFac);   // 2^E of each token
-  float* const vs = reinterpret_cast<float*>(sm + R::kVs);     // V's scales [block][token]
-  float* const vmax = reinterpret_cast<float*>(sm + R::kVmax);  // and their largest, per block
+  float* const vfac = reinterpret_cast<float*>(sm + R::kVs);    // of V, NaN left out
+  float* const vmax = reinterpret_cast<float*>(sm + R::kVmax);  // their largest
+  uint32_t* const vnan = reinterpret_cast<uint32_t*>(sm + R::kNan);   // [block]: tokens of which it is NaN
   int* const pos_k = reinterpret_cast<int*>(sm + R::kPos);       // positions of the tile's tokens (with slopes)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -249,12 +253,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
             make_uint4(pack_f16(q[k] * up, q[k + 1] * up), pack_f16(q[k + 2] * up, q[k + 3] * up),
                        pack_f16(q[k + 4] * up, q[k + 5] * up), pack_f16(q[k + 6] * up, q[k + 7] * up));
     }
-    float m = -INFINITY, l = 0.f, M[NB], rs[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      M[b] = -INFINITY;
-      rs[b] = 0.f;
-    }
+    float m = -INFINITY, l = 0.f, M = -INFINITY, rs = 0.f;
+    uint32_t poison = 0;   // bit b: the row sees a NaN of block b
     bool first = true;   // no tile of the unit is in O yet
 
     for (int it = 0; it < n_tiles; ++it) {
@@ -293,10 +293,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
 #pragma unroll
         for (int ab = 0; ab < 2; ++ab) {
           const int sh = 8 * ((g & 1) + 2 * ab), n = sub * 16 + 4 * (g >> 1) + (g & 1) + 2 * ab;
-          int top = 0;
+          float ke[NB], top = 0.f;   // 255: infinity, which turns the score into NaN
 #pragma unroll
-          for (int b = 0; b < NB; ++b) top = max(top, (int)(scw[b] >> sh & 255u));
-          if ((warp & 1) == 0 && c == 0) fac[n] = __uint_as_float((uint32_t)top << 23);   // 255: infinity
+          for (int b = 0; b < NB; ++b) {
+            ke[b] = __uint_as_float((scw[b] >> sh & 255u) << 23);
+            top = fmaxf(top, ke[b]);
+          }
+          if ((warp & 1) == 0 && c == 0) fac[n] = top;
 #pragma unroll
           for (int k = 0; k < UB; ++k) {
             uint32_t hc[4];
@@ -306,22 +309,36 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
             } else {
               codes_e2m1(w[k][ab], hc);
             }
-            const uint32_t own = UB == 2 ? (b0 ? scw[NB - 2 + k] : scw[k]) : (b0 ? scw[NB - 1] : scw[0]);
-            const int e = (int)(own >> sh & 255u);
-            const uint32_t s2 = pow2_f16x2(top - e);
+            const float own = ratio(b0 ? ke[NB - UB + k] : ke[k], top);
+            const uint32_t s2 = pack_f16(own, own);
             *reinterpret_cast<uint4*>(sm + R::kK + (n >> 3) * R::kKSbo + (4 * (b0 + k) + c) * R::kKLbo + (n & 7) * 16) =
                 make_uint4(mul_f16(hc[0], s2), mul_f16(hc[1], s2), mul_f16(hc[2], s2), mul_f16(hc[3], s2));
           }
         }
-        if (warp == 0 && lane < 8 * NB) {   // V's scales: word (quad, b)
-          const uint32_t z = reinterpret_cast<const uint32_t*>(sv + Tile::kScaleOff)[lane];
-          const float4 y = make_float4(scale_f32(z, 0), scale_f32(z, 1), scale_f32(z, 2), scale_f32(z, 3));
-          *reinterpret_cast<float4*>(vs + (lane % NB) * kMxTile + lane / NB * 4) = y;
-          float top = fmaxf(fmaxf(y.x, y.y), fmaxf(y.z, y.w));
+        if (warp == 3 && lane < 8) {   // V's factors: a lane has a quad of tokens
+          float top[4] = {0.f, 0.f, 0.f, 0.f};
+          uint32_t nan[NB];
 #pragma unroll
-          for (int d = NB; d < 8 * NB; d <<= 1) top = fmaxf(top, __shfl_xor_sync(NB == 4 ? 0xffffffffu : 0xffffu, top, d));
-          if (lane < NB) vmax[lane] = top;
+          for (int b = 0; b < NB; ++b) {
+            const uint32_t z = *reinterpret_cast<const uint32_t*>(sv + mx_scale_off<D, FMT>(lane, b));
+            nan[b] = 0;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const float y = scale_f32(z, t);
+              if (y == INFINITY) nan[b] |= 1u << (4 * lane + t);
+              else top[t] = fmaxf(top[t], y);
+            }
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1) nan[b] |= __shfl_xor_sync(0xffu, nan[b], d);
+            if (lane == 0) vnan[b] = nan[b];
+          }
+          *reinterpret_cast<float4*>(vfac + 4 * lane) = make_float4(top[0], top[1], top[2], top[3]);
+          float all = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+#pragma unroll
+          for (int d = 1; d < 8; d <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffu, all, d));
+          if (lane == 0) *vmax = all;
         }
+        __syncwarp();
         if (p.slopes && warp == 1) {
           const int j = tok0 + lane - rq.base;
           int at = tok0 + lane;
@@ -342,12 +359,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
             umma_ss(tmem + R::kS, smem_desc(smem_u32(sm + R::kQ) + k * 2 * R::kQLbo, R::kQLbo, R::kQSbo),
-                    smem_desc(smem_u32(sm + R::kK) + k * 2 * R::kKLbo, R::kKLbo, R::kKSbo), k > 0);
+                    smem_desc(smem_u32(sm + R::kK) + k * 2 * R::kKLbo, R::kKLbo, R::kKSbo), idesc(kMxTile), k > 0);
           umma_commit(smem_u32(bar_s));
         }
         busy_s = true;
         // ---- V, once the previous product has read its operands
         load_codes(sv);
+        const float4 ve = *reinterpret_cast<const float4*>(vfac + sub * 16 + 4 * c);   // of this lane's tokens
         if (busy_o) {
           lost |= !mbar_wait_bounded(smem_u32(bar_o), phase_o);
           phase_o ^= 1;
@@ -363,12 +381,17 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
             codes_e2m1(w[k][0], hv[0]);
             codes_e2m1(w[k][1], hv[2]);
           }
+          const uint32_t z = *reinterpret_cast<const uint32_t*>(sv + mx_scale_off<D, FMT>(sub * 4 + c, b0 + k));
+          float y[4] = {ratio(scale_f32(z, 0), ve.x), ratio(scale_f32(z, 1), ve.y), ratio(scale_f32(z, 2), ve.z),
+                        ratio(scale_f32(z, 3), ve.w)};
+          // (a NaN block's ratio is large: its codes are 0, and so is what it gives)
+          const uint32_t s01 = pack_f16(fminf(y[0], 1.f), fminf(y[1], 1.f)), s23 = pack_f16(fminf(y[2], 1.f), fminf(y[3], 1.f));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int r = 4 * g + j;
             *reinterpret_cast<uint2*>(sm + R::kV + (b0 + k) * R::kVBlock + (r >> 3) * R::kVSbo +
                                       (2 * sub + (c >> 1)) * R::kVLbo + (r & 7) * 16 + (c & 1) * 8) =
-                make_uint2(hv[j][0], hv[j][1]);
+                make_uint2(mul_f16(hv[j][0], s01), mul_f16(hv[j][1], s23));
           }
         }
         // ---- scores in log2 units
@@ -410,34 +433,29 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         }
 #pragma unroll
         for (int t = 0; t < 32; ++t) top = fmaxf(top, x[t]);
-        // ---- raise the references if a score or a weight could leave its range
-        bool over = top > m + kScoreSlack;
-        {
-          const float pm = ex2(top - (m == -INFINITY ? 0.f : m));
-#pragma unroll
-          for (int b = 0; b < NB; ++b) over |= pm * vmax[b] * rs[b] > kWeightMax;
+        if constexpr (NB == 4) {
+          const uint4 z = *reinterpret_cast<const uint4*>(vnan);
+          poison |= (z.x & vis ? 1u : 0u) | (z.y & vis ? 2u : 0u) | (z.z & vis ? 4u : 0u) | (z.w & vis ? 8u : 0u);
+        } else {
+          const uint2 z = *reinterpret_cast<const uint2*>(vnan);
+          poison |= (z.x & vis ? 1u : 0u) | (z.y & vis ? 2u : 0u);
         }
+        // ---- raise the references if a score or a weight could leave its range
+        const bool over = top > m + kScoreSlack || ex2(top - (m == -INFINITY ? 0.f : m)) * *vmax * rs > kWeightMax;
         if (__any_sync(0xffffffffu, over)) {   // (all lanes: the TMEM accesses are the warp's)
           const float mn = fmaxf(m, top);
           if (m != -INFINITY) l *= ex2(m - mn);
           m = mn;
+          float bm = -INFINITY;
+#pragma unroll
+          for (int t = 0; t < 32; ++t) bm = fmaxf(bm, x[t] + (float)((__float_as_int(vfac[t]) >> 23) - 127));
+          const float Mn = fmaxf(M, bm - kWeightExp);
+          const float back = M == -INFINITY ? 0.f : ex2(M - Mn);
+          M = Mn;
+          rs = Mn == -INFINITY ? 0.f : ex2(mn - Mn);
+          if (!first) {
 #pragma unroll 1
-          for (int b = 0; b < NB; ++b) {
-            float bm = -INFINITY;
-#pragma unroll
-            for (int t = 0; t < 32; ++t)
-              bm = fmaxf(bm, x[t] + (float)((int)(__float_as_uint(vs[b * kMxTile + t]) >> 23) - 127));
-            float Mb = 0.f;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) Mb = i == b ? M[i] : Mb;
-            const float Mn = fmaxf(Mb, bm - kWeightExp);
-            const float back = Mb == -INFINITY ? 0.f : ex2(Mb - Mn), r = Mn == -INFINITY ? 0.f : ex2(mn - Mn);
-#pragma unroll
-            for (int i = 0; i < NB; ++i) {
-              M[i] = i == b ? Mn : M[i];
-              rs[i] = i == b ? r : rs[i];
-            }
-            if (!first) {
+            for (int b = 0; b < NB; ++b) {
               float o[32];
               tmem_ld32(mine + R::kO + 32 * b, o);
 #pragma unroll
@@ -449,36 +467,22 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         // ---- weights
         {
           const float mi = m == -INFINITY ? 0.f : m;
+          const float2 r2 = make_float2(rs, rs);
           float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int t = 0; t < 32; t += 2) {
-            x[t] = ex2(x[t] - mi);
-            x[t + 1] = ex2(x[t + 1] - mi);
-            sum.x += x[t];
-            sum.y += x[t + 1];
-          }
-          l += sum.x + sum.y;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
           uint32_t pw[16];
-          const float2 r2 = make_float2(rs[b], rs[b]);
 #pragma unroll
           for (int t = 0; t < 32; t += 4) {
-            const float4 sc = *reinterpret_cast<const float4*>(vs + b * kMxTile + t);
-            float2 y = mul2(mul2(make_float2(x[t], x[t + 1]), make_float2(sc.x, sc.y)), r2);
-            float2 z = mul2(mul2(make_float2(x[t + 2], x[t + 3]), make_float2(sc.z, sc.w)), r2);
-            if (edge) {   // 0 times the infinity that marks a block of NaN
-              if (!(vis >> t & 1)) y.x = 0.f;
-              if (!(vis >> t & 2)) y.y = 0.f;
-              if (!(vis >> t & 4)) z.x = 0.f;
-              if (!(vis >> t & 8)) z.y = 0.f;
-            }
-            pw[t / 2] = pack_f16(y.x, y.y);
-            pw[t / 2 + 1] = pack_f16(z.x, z.y);
+            const float2 y = make_float2(ex2(x[t] - mi), ex2(x[t + 1] - mi));
+            const float2 z = make_float2(ex2(x[t + 2] - mi), ex2(x[t + 3] - mi));
+            sum = add2(sum, add2(y, z));
+            const float4 sc = *reinterpret_cast<const float4*>(vfac + t);
+            const float2 wy = mul2(mul2(y, make_float2(sc.x, sc.y)), r2), wz = mul2(mul2(z, make_float2(sc.z, sc.w)), r2);
+            pw[t / 2] = pack_f16(wy.x, wy.y);
+            pw[t / 2 + 1] = pack_f16(wz.x, wz.y);
           }
+          l += sum.x + sum.y;
           __syncwarp();
-          tmem_st16(mine + R::kP + 16 * b, pw);
+          tmem_st16(mine + R::kP, pw);
         }
         tmem_wait_st();
         fence_proxy_async();
@@ -490,12 +494,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         if (tid == 0) {
           tmem_after();
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              umma_ts(tmem + R::kO + 32 * b, tmem + R::kP + 16 * b + 8 * k,
-                      smem_desc(smem_u32(sm + R::kV) + b * R::kVBlock + k * 2 * R::kVLbo, R::kVLbo, R::kVSbo),
-                      !(first && k == 0));
+          for (int k = 0; k < 2; ++k)
+            umma_ts(tmem + R::kO, tmem + R::kP + 8 * k,
+                    smem_desc(smem_u32(sm + R::kV) + k * 2 * R::kVLbo, R::kVLbo, R::kVSbo), idesc(D), !(first && k == 0));
           umma_commit(smem_u32(bar_o));
         }
         busy_o = true;
@@ -537,9 +538,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
       float o[32];
       tmem_ld32(mine + R::kO + 32 * b, o);
       // a row that saw only NaN has no M: its l is NaN
-      const float fb = M[b] == -INFINITY ? l : ex2(M[b] - m) * inv;
+      const float fb = poison >> b & 1 ? NAN : M == -INFINITY ? l : ex2(M - m) * inv;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = first ? l : o[i] * fb;
+      for (int i = 0; i < 32; ++i) o[i] = first ? 0.f : o[i] * fb;
       if (there && !whole) {
 #pragma unroll
         for (int i = 0; i < 32; i += 4)
