@@ -14,8 +14,9 @@
 // an element is rounded to 2^-24 of 2^E, which is less than 2^-26 of its token's
 // largest element.  A block of NaN counts as 0 in V' and is put into the outputs
 // of the rows that see it at the end.
-// All threads convert K' while the previous tile's P V runs, and V while the
-// scores are computed; two blocks per SM fill each other's waits.
+// Four warps convert codes and issue copies and products, four compute the
+// softmax; operands, scores and weights are double-buffered, so that tile i's
+// softmax, tile i + 1's scores and the product P V of tile i - 1 run together.
 //
 // Operands in shared memory are K-major without swizzle: core matrices of 8
 // rows x 16 bytes, at (row / 8) * SBO + (k / 8) * LBO.  LBO and SBO are padded so
@@ -26,7 +27,7 @@
 namespace loopvq {
 namespace {
 
-constexpr int kRowsThreads = kMxRowsChunk;
+constexpr int kRowsThreads = 2 * kMxRowsChunk;   // softmax, conversion
 
 template <int D, int FMT>
 struct Rows {
@@ -36,14 +37,29 @@ struct Rows {
   static constexpr int kQLbo = 128, kQSbo = D / 8 * 128;                 // rows x channels
   static constexpr int kKLbo = 160, kKSbo = D / 8 * 160;                 // tokens x channels
   static constexpr int kVLbo = 144, kVSbo = 672, kVBlock = 4 * kVSbo;    // channels x tokens, per block
-  static constexpr int kQ = 0, kK = kQ + kMxRowsChunk / 8 * kQSbo, kV = kK + kMxTile / 8 * kKSbo,
-                       kRing = kV + NB * kVBlock, kSlot = 2 * Tile::kBytes, kFac = kRing + kStages * kSlot,
-                       kVs = kFac + kMxTile * 4, kNan = kVs + kMxTile * 4, kVmax = kNan + 16, kPos = kVmax + 16, kBars = kPos + kMxTile * 4,
-                       kNeed = kBars + (kStages + 2) * 8 + 16;
+  static constexpr int kKBuf = kMxTile / 8 * kKSbo, kVBuf = NB * kVBlock;
+  static constexpr int kQ = 0, kK = kQ + kMxRowsChunk / 8 * kQSbo, kV = kK + 2 * kKBuf, kRing = kV + 2 * kVBuf,
+                       kSlot = 2 * Tile::kBytes, kInfo = kRing + kStages * kSlot;
+  static constexpr int kNeed = kInfo + 1024;
   static constexpr int kBytes = kNeed > 76 * 1024 ? kNeed : 76 * 1024;   // two blocks per SM, no third that would wait for TMEM
-  // TMEM columns: O, S, P
-  static constexpr int kO = 0, kS = D, kP = D + kMxTile, kCols = D == 128 ? 256 : 128;
-  static_assert(kP + 16 <= kCols, "TMEM");
+  // TMEM columns: O, S twice, P twice
+  static constexpr int kO = 0, kS = D, kP = D + 2 * kMxTile, kCols = 256;
+  static_assert(kP + 32 <= kCols, "TMEM");
+};
+// What the converting warps tell the others: per tile in turn, and barriers.
+struct RowsInfo {
+  struct alignas(16) {
+    float fac[kMxTile];    // 2^E of each key
+    float vfac[kMxTile];   // of each value, NaN left out
+    int pos[kMxTile];      // positions (with slopes)
+    uint32_t nan[4];       // [block]: tokens whose value is NaN there
+    float vmax;            // largest of vfac
+    uint32_t hidden;       // the page is not in the pool
+  } t[2];
+  uint64_t full[4];                               // raw tiles
+  uint64_t told[2], scores[2], weights[2], sums[2];   // info written; S, P, O += P V done
+  uint64_t query;                                 // Q written
+  uint32_t tmem, bad;
 };
 
 __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -87,18 +103,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32]) {
-  uint32_t r[32];
-#pragma unroll
-  for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(v[i]);
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float (&v)[16]) {
+  uint32_t r[16];
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
       : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
   asm volatile(
@@ -124,16 +139,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
   using Tile = MxTile<D, FMT>;
   constexpr int NB = R::NB, S = R::kStages, CHUNK = kMxRowsChunk;
   extern __shared__ __align__(1024) uint8_t sm[];
-  uint64_t* const full = reinterpret_cast<uint64_t*>(sm + R::kBars);
-  uint64_t* const bar_s = full + S;   // scores done
-  uint64_t* const bar_o = bar_s + 1;  // P V done
-  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(bar_o + 1);
-  float* const fac = reinterpret_cast<float*>(sm + R::kFac);   // 2^E of each token
-  float* const vfac = reinterpret_cast<float*>(sm + R::kVs);    // of V, NaN left out
-  float* const vmax = reinterpret_cast<float*>(sm + R::kVmax);  // their largest
-  uint32_t* const vnan = reinterpret_cast<uint32_t*>(sm + R::kNan);   // [block]: tokens of which it is NaN
-  int* const pos_k = reinterpret_cast<int*>(sm + R::kPos);       // positions of the tile's tokens (with slopes)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  static_assert(sizeof(RowsInfo) <= 1024 && S <= 4, "");
+  RowsInfo& I = *reinterpret_cast<RowsInfo*>(sm + R::kInfo);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   // this block's share of the list of tiles
@@ -152,144 +160,139 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
   const int extra = (int)(total % p.n_workers);
   const int64_t begin = wid * share + min(wid, extra);
   const int count = (int)share + (wid < extra);
-  if (tid == 0) p.headers[wid] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0) p.headers[wid] = make_int4(0, 0, 0, 0);
   if (count == 0) return;   // the whole block
   MxCursor cc = mx_seek<CHUNK>(p, begin, u0, t0, lane);
 
   if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(R::kCols));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&I.tmem)), "r"(R::kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (tid == 0) {
-    for (int i = 0; i < S + 2; ++i) mbar_init(smem_u32(full + i), 1);
+  if (threadIdx.x == 128) {
+    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&I.full[i]), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&I.told[i]), 4);
+      mbar_init(smem_u32(&I.scores[i]), 1);
+      mbar_init(smem_u32(&I.weights[i]), 128);
+      mbar_init(smem_u32(&I.sums[i]), 1);
+    }
+    mbar_init(smem_u32(&I.query), 128);
+    I.bad = 0;
     fence_mbar_init();
   }
   tmem_before();
   __syncthreads();
   tmem_after();
-  const uint32_t tmem = *tmem_slot;
-  const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);   // this warp's lanes
+  const uint32_t tmem = I.tmem;
+  // Use n of a barrier that alternates between two: its parity.
+  auto wait2 = [&](uint64_t* bars, int n) { return mbar_wait_bounded(smem_u32(bars + (n & 1)), (uint32_t)(n >> 1) & 1); };
+  bool ok = true;   // no wait has run out
+  int done = 0;     // tiles
 
-  MxCursor pc = cc;   // thread 0 feeds the ring; all threads keep its place
-  const int per = p.L.page_tokens / kMxTile;
-  int page = pc.t / per, in_page = pc.t % per, issued = 0;
-  uint32_t bad = 0;   // bit per slot: its tile's page is not in the pool
-  int64_t head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
-  int id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
-  auto issue = [&](int slot) {
-    const bool ok = id >= 0 && id < p.L.n_pages;
-    bad = (bad & ~(1u << slot)) | (ok ? 0u : 1u << slot);
-    if (tid == 0) {
-      const uint32_t bar = smem_u32(full + slot), dst = smem_u32(sm + R::kRing + slot * R::kSlot);
-      if (ok) {
+  if (warp >= 4) {
+    // ======================== conversion, copies, products
+    const int w4 = warp - 4;
+    const bool leader = threadIdx.x == 128;
+    const int sub = w4 >> 1;
+    constexpr int UB = NB / 2;   // blocks of a warp, of one half of the tile
+    const int b0 = (w4 & 1) * UB;
+    MxCursor pc = cc;            // the leader's: the next tile to copy
+    const int per = p.L.page_tokens / kMxTile;
+    int page = pc.t / per, in_page = pc.t % per, issued = 0;
+    int64_t head = 0;
+    int id = 0;
+    if (leader) {
+      head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
+      id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+    }
+    auto issue = [&]() {   // by the leader
+      const int slot = issued % S;
+      const uint32_t bar = smem_u32(&I.full[slot]), dst = smem_u32(sm + R::kRing + slot * R::kSlot);
+      if (id >= 0 && id < p.L.n_pages) {
         const int64_t at = (head + (int64_t)id * per + in_page) * Tile::kBytes;
         mbar_arrive_expect_tx(bar, 2 * Tile::kBytes);
         bulk_g2s(dst, p.pk + at, Tile::kBytes, bar);
         bulk_g2s(dst + Tile::kBytes, p.pv + at, Tile::kBytes, bar);
       } else {
         set_fault(p.fault, LOOPVQ_FAULT_POOL_RANGE);
+        atomicOr(&I.bad, 1u << slot);   // before the arrival that publishes it
         mbar_arrive(bar);
       }
-    }
-    if (++issued < count) {
-      if (++pc.t == pc.tiles) {
-        mx_next_unit<CHUNK>(p, &pc);
-        page = in_page = 0;
-        head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
-        id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages);
-      } else if (++in_page == per) {
-        in_page = 0;
-        ++page;
-        id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+      if (++issued < count) {
+        if (++pc.t == pc.tiles) {
+          mx_next_unit<CHUNK>(p, &pc);
+          page = in_page = 0;
+          head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
+          id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages);
+        } else if (++in_page == per) {
+          in_page = 0;
+          ++page;
+          id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+        }
       }
-    }
-  };
-  for (int i = 0; i < S && i < count; ++i) issue(i);
-
-  int done = 0, slot = 0;
-  uint32_t phase = 0, phase_s = 0, phase_o = 0;
-  bool busy_o = false;   // a P V is on its way
-  bool busy_s = false;
-  bool lost = false;
-  while (done < count && !lost) {
-    MxReq rq = {};
-    mx_request(p.L, cc.r, &rq, nullptr);
-    const int chunks = cc.units / p.H, h = cc.u / chunks, rho0 = (cc.u - h * chunks) * CHUNK;
-    const int rows = min(CHUNK, rq.n * p.G - rho0);
-    const int first_tile = cc.t, n_tiles = min(cc.tiles - cc.t, count - done);
-    const uint64_t all_new = rq.n >= 64 ? ~0ull : (1ull << rq.n) - 1;
-
-    // this thread's row: scaled by a power of two to a largest magnitude in
-    // [2^14, 2^15), as fp16 (exact for bf16 down to 2^-28 of it)
-    const int rho = rho0 + tid;
-    const bool there = tid < rows;
-    float f, slope = 0.f;
-    uint64_t sees = 0;
-    int pos_q = 0;
-    {
-      const int node = rho / p.G, hq = h * p.G + rho % p.G;
-      float q[D];
-      float mx = 0.f;
-      if (there) {
-        const int64_t at = (int64_t)(rq.row0 + node) * p.qn + (int64_t)hq * p.qh;
+    };
+    if (leader)
+      for (int i = 0; i < S && i < count; ++i) issue();
+    // Barrier of these warps; false, in all threads alike, once a wait has run out in any.
+    auto sync4 = [&]() {
+      uint32_t failed;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+          : "=r"(failed)
+          : "r"(ok ? 0u : 1u)
+          : "memory");
+      return ok = failed == 0;
+    };
+    bool go = true;
+    int units = 0;
+    // O += P V of tile i, once its weights are there
+    auto product = [&](int i, bool fresh) {
+      ok &= wait2(I.weights, i);
+      if (leader) {
+        tmem_after();
 #pragma unroll
-        for (int k = 0; k < D; k += 8) load_query<__nv_bfloat16>(p.q, at + k, p.q_vec, q + k);
-        sees = (p.tree_mask ? __ldg(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
-        pos_q = rq.base + __popcll(sees & ~(1ull << node));
-        if (p.slopes) slope = __ldg(p.slopes + hq) * kLog2e;
-      } else {
-#pragma unroll
-        for (int k = 0; k < D; ++k) q[k] = 0.f;
+        for (int k = 0; k < 2; ++k)
+          umma_ts(tmem + R::kO, tmem + R::kP + 16 * (i & 1) + 8 * k,
+                  smem_desc(smem_u32(sm + R::kV) + (i & 1) * R::kVBuf + k * 2 * R::kVLbo, R::kVLbo, R::kVSbo), idesc(D),
+                  !(fresh && k == 0));
+        umma_commit(smem_u32(&I.sums[i & 1]));
       }
-#pragma unroll
-      for (int k = 0; k < D; ++k) mx = fmaxf(mx, fabsf(q[k]));
-      const int ex = max((int)(__float_as_uint(mx) >> 23), 1) - 127;
-      const int k2 = min(14 - ex, 120);
-      const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
-      f = p.softcap > 0.f ? p.scale / p.softcap * down : p.scale * kLog2e * down;
-#pragma unroll
-      for (int k = 0; k < D; k += 8)
-        *reinterpret_cast<uint4*>(sm + R::kQ + (tid >> 3) * R::kQSbo + (k >> 3) * R::kQLbo + (tid & 7) * 16) =
-            make_uint4(pack_f16(q[k] * up, q[k + 1] * up), pack_f16(q[k + 2] * up, q[k + 3] * up),
-                       pack_f16(q[k + 4] * up, q[k + 5] * up), pack_f16(q[k + 6] * up, q[k + 7] * up));
-    }
-    float m = -INFINITY, l = 0.f, M = -INFINITY, rs = 0.f;
-    uint32_t poison = 0;   // bit b: the row sees a NaN of block b
-    bool first = true;   // no tile of the unit is in O yet
-
-    for (int it = 0; it < n_tiles; ++it) {
-      const int tok0 = (first_tile + it) * kMxTile;
-      const bool edge = tok0 + kMxTile > rq.base;
-      const bool skip = bad >> slot & 1;
-      lost |= !mbar_wait_bounded(smem_u32(full + slot), phase);
-      const uint8_t* const sk = sm + R::kRing + slot * R::kSlot;
-      const uint8_t* const sv = sk + Tile::kBytes;
-      if (!skip) {
-        // ---- K', and the factors of scores and weights.  A warp converts half a tile of two blocks (D = 64: of one).
-        const int sub = warp >> 1;
-        constexpr int UB = NB / 2;   // blocks of a warp
-        const int b0 = (warp & 1) * UB;
-        uint32_t w[UB][4] = {};      // e4m3: 4 words of a block; e2m1: 2
+    };
+    while (done < count && go) {
+      MxReq rq = {};
+      mx_request(p.L, cc.r, &rq, nullptr);
+      const int first_tile = cc.t, n_tiles = min(cc.tiles - cc.t, count - done);
+      const uint64_t all_new = rq.n >= 64 ? ~0ull : (1ull << rq.n) - 1;
+      for (int it = 0; it < n_tiles; ++it) {
+        const int i = done, slot = i % S;
+        auto& T = I.t[i & 1];
+        const int tok0 = (first_tile + it) * kMxTile;
+        const bool edge = tok0 + kMxTile > rq.base;
+        ok &= mbar_wait_bounded(smem_u32(&I.full[slot]), (uint32_t)(i / S) & 1);
+        const bool bad = *reinterpret_cast<volatile uint32_t*>(&I.bad) >> slot & 1;
+        if (i >= 2) ok &= wait2(I.scores, i - 2);   // K' of tile i - 2 has been read
+        const uint8_t* const sk = sm + R::kRing + slot * R::kSlot;
+        const uint8_t* const sv = sk + Tile::kBytes;
+        uint32_t w[UB][4];   // e4m3: 4 words of a block; e2m1: 2
         auto load_codes = [&](const uint8_t* tile) {
-          if constexpr (FMT == LOOPVQ_MX_E4M3) {
 #pragma unroll
-            for (int k = 0; k < UB; ++k) {
+          for (int k = 0; k < UB; ++k) {
+            if constexpr (FMT == LOOPVQ_MX_E4M3) {
               const uint4 z = *reinterpret_cast<const uint4*>(tile + mx_code_off<D, FMT>(sub, b0 + k, lane));
               w[k][0] = z.x; w[k][1] = z.y; w[k][2] = z.z; w[k][3] = z.w;
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < UB; ++k) {
+            } else {
               const uint2 z = *reinterpret_cast<const uint2*>(tile + mx_code_off<D, FMT>(sub, b0 + k, lane));
-              w[k][0] = z.x; w[k][1] = z.y;
+              w[k][0] = z.x; w[k][1] = z.y; w[k][2] = w[k][3] = 0;
             }
+            if (bad) w[k][0] = w[k][1] = w[k][2] = w[k][3] = 0;
           }
         };
+        // ---- K'
         load_codes(sk);
-        const int quad = sub * 4 + (g >> 1);
         uint32_t scw[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) scw[b] = *reinterpret_cast<const uint32_t*>(sk + mx_scale_off<D, FMT>(quad, b));
+        for (int b = 0; b < NB; ++b) scw[b] = *reinterpret_cast<const uint32_t*>(sk + mx_scale_off<D, FMT>(sub * 4 + (g >> 1), b));
+        uint8_t* const dk = sm + R::kK + (i & 1) * R::kKBuf;
 #pragma unroll
         for (int ab = 0; ab < 2; ++ab) {
           const int sh = 8 * ((g & 1) + 2 * ab), n = sub * 16 + 4 * (g >> 1) + (g & 1) + 2 * ab;
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
             ke[b] = __uint_as_float((scw[b] >> sh & 255u) << 23);
             top = fmaxf(top, ke[b]);
           }
-          if ((warp & 1) == 0 && c == 0) fac[n] = top;
+          if ((w4 & 1) == 0 && c == 0) T.fac[n] = top;
 #pragma unroll
           for (int k = 0; k < UB; ++k) {
             uint32_t hc[4];
@@ -311,66 +314,62 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
             }
             const float own = ratio(b0 ? ke[NB - UB + k] : ke[k], top);
             const uint32_t s2 = pack_f16(own, own);
-            *reinterpret_cast<uint4*>(sm + R::kK + (n >> 3) * R::kKSbo + (4 * (b0 + k) + c) * R::kKLbo + (n & 7) * 16) =
+            *reinterpret_cast<uint4*>(dk + (n >> 3) * R::kKSbo + (4 * (b0 + k) + c) * R::kKLbo + (n & 7) * 16) =
                 make_uint4(mul_f16(hc[0], s2), mul_f16(hc[1], s2), mul_f16(hc[2], s2), mul_f16(hc[3], s2));
           }
         }
-        if (warp == 3 && lane < 8) {   // V's factors: a lane has a quad of tokens
+        if (w4 == 3 && lane < 8) {   // V's factors: a lane has a quad of tokens
           float top[4] = {0.f, 0.f, 0.f, 0.f};
-          uint32_t nan[NB];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const uint32_t z = *reinterpret_cast<const uint32_t*>(sv + mx_scale_off<D, FMT>(lane, b));
-            nan[b] = 0;
+            uint32_t nan = 0;
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
               const float y = scale_f32(z, t);
-              if (y == INFINITY) nan[b] |= 1u << (4 * lane + t);
+              if (y == INFINITY) nan |= 1u << (4 * lane + t);
               else top[t] = fmaxf(top[t], y);
             }
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) nan[b] |= __shfl_xor_sync(0xffu, nan[b], d);
-            if (lane == 0) vnan[b] = nan[b];
+            for (int d = 1; d < 8; d <<= 1) nan |= __shfl_xor_sync(0xffu, nan, d);
+            if (lane == 0) T.nan[b] = nan;
           }
-          *reinterpret_cast<float4*>(vfac + 4 * lane) = make_float4(top[0], top[1], top[2], top[3]);
+          *reinterpret_cast<float4*>(T.vfac + 4 * lane) = make_float4(top[0], top[1], top[2], top[3]);
           float all = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
 #pragma unroll
           for (int d = 1; d < 8; d <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffu, all, d));
-          if (lane == 0) *vmax = all;
+          if (lane == 0) {
+            T.vmax = all;
+            T.hidden = bad;
+          }
         }
-        __syncwarp();
-        if (p.slopes && warp == 1) {
+        if (p.slopes && w4 == 1) {
           const int j = tok0 + lane - rq.base;
           int at = tok0 + lane;
           if (j >= 0 && j < rq.n) {
             const uint64_t its = p.tree_mask ? __ldg(p.tree_mask + rq.row0 + j) & all_new : (2ull << j) - 1;
             at = rq.base + __popcll(its & ~(1ull << j));
           }
-          pos_k[lane] = at;
+          T.pos[lane] = at;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&I.told[i & 1]));
         fence_proxy_async();
-        tmem_before();
-        if (__syncthreads_or(lost)) {
-          lost = true;
-          break;
-        }
-        if (tid == 0) {
+        if (!(go = sync4())) break;
+        if (leader) {
+          if (it == 0) ok &= mbar_wait_bounded(smem_u32(&I.query), (uint32_t)units & 1);
           tmem_after();
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            umma_ss(tmem + R::kS, smem_desc(smem_u32(sm + R::kQ) + k * 2 * R::kQLbo, R::kQLbo, R::kQSbo),
-                    smem_desc(smem_u32(sm + R::kK) + k * 2 * R::kKLbo, R::kKLbo, R::kKSbo), idesc(kMxTile), k > 0);
-          umma_commit(smem_u32(bar_s));
+            umma_ss(tmem + R::kS + (i & 1) * kMxTile, smem_desc(smem_u32(sm + R::kQ) + k * 2 * R::kQLbo, R::kQLbo, R::kQSbo),
+                    smem_desc(smem_u32(dk) + k * 2 * R::kKLbo, R::kKLbo, R::kKSbo), idesc(kMxTile), k > 0);
+          umma_commit(smem_u32(&I.scores[i & 1]));
         }
-        busy_s = true;
-        // ---- V, once the previous product has read its operands
+        // ---- V'
         load_codes(sv);
-        const float4 ve = *reinterpret_cast<const float4*>(vfac + sub * 16 + 4 * c);   // of this lane's tokens
-        if (busy_o) {
-          lost |= !mbar_wait_bounded(smem_u32(bar_o), phase_o);
-          phase_o ^= 1;
-          busy_o = false;
-        }
+        const float4 ve = *reinterpret_cast<const float4*>(T.vfac + sub * 16 + 4 * c);   // of this lane's tokens
+        if (i >= 2) ok &= wait2(I.sums, i - 2);   // V' of tile i - 2 has been read
+        uint8_t* const dv = sm + R::kV + (i & 1) * R::kVBuf;
 #pragma unroll
         for (int k = 0; k < UB; ++k) {
           uint32_t hv[4][2];   // [channel j][token pair]
@@ -381,33 +380,115 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
             codes_e2m1(w[k][0], hv[0]);
             codes_e2m1(w[k][1], hv[2]);
           }
+          // a NaN block's ratio is large: its codes are 0, and so is what it gives
           const uint32_t z = *reinterpret_cast<const uint32_t*>(sv + mx_scale_off<D, FMT>(sub * 4 + c, b0 + k));
-          float y[4] = {ratio(scale_f32(z, 0), ve.x), ratio(scale_f32(z, 1), ve.y), ratio(scale_f32(z, 2), ve.z),
-                        ratio(scale_f32(z, 3), ve.w)};
-          // (a NaN block's ratio is large: its codes are 0, and so is what it gives)
-          const uint32_t s01 = pack_f16(fminf(y[0], 1.f), fminf(y[1], 1.f)), s23 = pack_f16(fminf(y[2], 1.f), fminf(y[3], 1.f));
+          const uint32_t s01 = pack_f16(fminf(ratio(scale_f32(z, 0), ve.x), 1.f), fminf(ratio(scale_f32(z, 1), ve.y), 1.f));
+          const uint32_t s23 = pack_f16(fminf(ratio(scale_f32(z, 2), ve.z), 1.f), fminf(ratio(scale_f32(z, 3), ve.w), 1.f));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int r = 4 * g + j;
-            *reinterpret_cast<uint2*>(sm + R::kV + (b0 + k) * R::kVBlock + (r >> 3) * R::kVSbo +
-                                      (2 * sub + (c >> 1)) * R::kVLbo + (r & 7) * 16 + (c & 1) * 8) =
+            *reinterpret_cast<uint2*>(dv + (b0 + k) * R::kVBlock + (r >> 3) * R::kVSbo + (2 * sub + (c >> 1)) * R::kVLbo +
+                                      (r & 7) * 16 + (c & 1) * 8) =
                 make_uint2(mul_f16(hv[j][0], s01), mul_f16(hv[j][1], s23));
           }
         }
-        // ---- scores in log2 units
-        lost |= !mbar_wait_bounded(smem_u32(bar_s), phase_s);
-        phase_s ^= 1;
-        busy_s = false;
-        __syncwarp();
+        fence_proxy_async();
+        if (!(go = sync4())) break;   // the raw tile has been read, V' is written
+        if (leader) {
+          if (bad) atomicAnd(&I.bad, ~(1u << slot));
+          if (issued < count) issue();
+        }
+        if (it > 0) product(i - 1, it == 1);
+        if (it == n_tiles - 1) product(i, it == 0);
+        ++done;
+      }
+      ++units;
+      if (done < count && go) mx_next_unit<CHUNK>(p, &cc);
+    }
+    if (!ok && lane == 0) set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
+    if (leader && !ok)   // copies that are still on their way end before the block does
+      for (int i = max(0, issued - S); i < issued; ++i) mbar_wait_bounded(smem_u32(&I.full[i % S]), (uint32_t)(i / S) & 1);
+  } else {
+    // ======================== softmax: a thread has a row
+    const int tid = threadIdx.x;
+    const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);   // this warp's lanes
+    while (done < count && ok) {
+      MxReq rq = {};
+      mx_request(p.L, cc.r, &rq, nullptr);
+      const int chunks = cc.units / p.H, h = cc.u / chunks, rho0 = (cc.u - h * chunks) * CHUNK;
+      const int rows = min(CHUNK, rq.n * p.G - rho0);
+      const int first_tile = cc.t, n_tiles = min(cc.tiles - cc.t, count - done);
+      const uint64_t all_new = rq.n >= 64 ? ~0ull : (1ull << rq.n) - 1;
+      // the row: scaled by a power of two to a largest magnitude in [2^14, 2^15),
+      // as fp16 (exact for bf16 down to 2^-28 of it).  The last unit's scores are
+      // done: nothing reads Q any more.
+      const int rho = rho0 + tid;
+      const bool there = tid < rows;
+      float f, slope = 0.f;
+      uint64_t sees = 0;
+      int pos_q = 0;
+      {
+        const int node = rho / p.G, hq = h * p.G + rho % p.G;
+        const __nv_bfloat16* x =
+            reinterpret_cast<const __nv_bfloat16*>(p.q) + (int64_t)(rq.row0 + node) * p.qn + (int64_t)hq * p.qh;
+        float mx = 0.f;
+        uint32_t q[D / 2];
+#pragma unroll
+        for (int k = 0; k < D / 2; ++k) q[k] = 0u;
+        if (there) {
+          if (p.q_vec) {
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) {
+              const uint4 z = __ldg(reinterpret_cast<const uint4*>(x) + k);
+              q[4 * k] = z.x; q[4 * k + 1] = z.y; q[4 * k + 2] = z.z; q[4 * k + 3] = z.w;
+            }
+          } else {
+            const uint16_t* x16 = reinterpret_cast<const uint16_t*>(x);
+#pragma unroll
+            for (int k = 0; k < D / 2; ++k) q[k] = (uint32_t)x16[2 * k] | (uint32_t)x16[2 * k + 1] << 16;
+          }
+          sees = (p.tree_mask ? __ldg(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
+          pos_q = rq.base + __popcll(sees & ~(1ull << node));
+          if (p.slopes) slope = __ldg(p.slopes + hq) * kLog2e;
+        }
+#pragma unroll
+        for (int k = 0; k < D / 2; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(q[k])), fabsf(bf16_hi(q[k]))));
+        const int ex = max((int)(__float_as_uint(mx) >> 23), 1) - 127;
+        const int k2 = min(14 - ex, 120);
+        const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
+        f = p.softcap > 0.f ? p.scale / p.softcap * down : p.scale * kLog2e * down;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          uint32_t z[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[j] = pack_f16(bf16_lo(q[4 * k + j]) * up, bf16_hi(q[4 * k + j]) * up);
+          *reinterpret_cast<uint4*>(sm + R::kQ + (tid >> 3) * R::kQSbo + k * R::kQLbo + (tid & 7) * 16) =
+              make_uint4(z[0], z[1], z[2], z[3]);
+        }
+      }
+      fence_proxy_async();
+      mbar_arrive(smem_u32(&I.query));
+
+      float m = -INFINITY, l = 0.f, M = -INFINITY, rs = 0.f;
+      uint32_t poison = 0;   // bit b: the row sees a NaN of block b
+      for (int it = 0; it < n_tiles; ++it) {
+        const int i = done + it;
+        const auto& T = I.t[i & 1];
+        const int tok0 = (first_tile + it) * kMxTile;
+        ok &= wait2(I.told, i);
+        ok &= wait2(I.scores, i);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         tmem_after();
+        const bool hidden = T.hidden != 0, edge = hidden || tok0 + kMxTile > rq.base;
         float x[32];
-        tmem_ld32(mine + R::kS, x);
-        float top = -INFINITY;
+        tmem_ld32(mine + R::kS + (i & 1) * kMxTile, x);
+        const float2 f2 = make_float2(f, f);
 #pragma unroll
         for (int t = 0; t < 32; t += 4) {
-          const float4 fc = *reinterpret_cast<const float4*>(fac + t);
-          const float2 a = mul2(mul2(make_float2(x[t], x[t + 1]), make_float2(f, f)), make_float2(fc.x, fc.y));
-          const float2 b = mul2(mul2(make_float2(x[t + 2], x[t + 3]), make_float2(f, f)), make_float2(fc.z, fc.w));
+          const float4 fc = *reinterpret_cast<const float4*>(T.fac + t);
+          const float2 a = mul2(mul2(make_float2(x[t], x[t + 1]), f2), make_float2(fc.x, fc.y));
+          const float2 b = mul2(mul2(make_float2(x[t + 2], x[t + 3]), f2), make_float2(fc.z, fc.w));
           x[t] = a.x;
           x[t + 1] = a.y;
           x[t + 2] = b.x;
@@ -417,162 +498,144 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
 #pragma unroll
           for (int t = 0; t < 32; ++t) x[t] = p.softcap * kLog2e * tanh_abs(x[t]);
         }
-        uint32_t vis = ~0u;
-        if (edge) {   // bits of the tokens that the row sees
-          const int lo = rq.base - tok0;   // the prefix's part of the tile, < 32
-          vis = lo > 0 ? ((1u << lo) - 1) | (uint32_t)(sees << lo) : (uint32_t)(lo > -64 ? sees >> -lo : 0ull);
-        }
         if (p.slopes) {
 #pragma unroll
-          for (int t = 0; t < 32; ++t) x[t] -= slope * (float)(pos_q - pos_k[t]);
+          for (int t = 0; t < 32; ++t) x[t] -= slope * (float)(pos_q - T.pos[t]);
         }
+        uint32_t vis = ~0u;   // bits of the tokens that the row sees
         if (edge) {
+          const int lo = rq.base - tok0;   // the prefix's part of the tile
+          vis = hidden ? 0u
+                : lo >= 32 ? ~0u
+                : lo > 0   ? ((1u << lo) - 1) | (uint32_t)(sees << lo)
+                           : (uint32_t)(lo > -64 ? sees >> -lo : 0ull);
 #pragma unroll
           for (int t = 0; t < 32; ++t)
             if (!(vis >> t & 1)) x[t] = -INFINITY;
         }
-#pragma unroll
-        for (int t = 0; t < 32; ++t) top = fmaxf(top, x[t]);
         if constexpr (NB == 4) {
-          const uint4 z = *reinterpret_cast<const uint4*>(vnan);
+          const uint4 z = *reinterpret_cast<const uint4*>(T.nan);
           poison |= (z.x & vis ? 1u : 0u) | (z.y & vis ? 2u : 0u) | (z.z & vis ? 4u : 0u) | (z.w & vis ? 8u : 0u);
         } else {
-          const uint2 z = *reinterpret_cast<const uint2*>(vnan);
+          const uint2 z = *reinterpret_cast<const uint2*>(T.nan);
           poison |= (z.x & vis ? 1u : 0u) | (z.y & vis ? 2u : 0u);
         }
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 32; ++t) top = fmaxf(top, x[t]);
         // ---- raise the references if a score or a weight could leave its range
-        const bool over = top > m + kScoreSlack || ex2(top - (m == -INFINITY ? 0.f : m)) * *vmax * rs > kWeightMax;
+        const bool over = top > m + kScoreSlack || ex2(top - (m == -INFINITY ? 0.f : m)) * T.vmax * rs > kWeightMax;
         if (__any_sync(0xffffffffu, over)) {   // (all lanes: the TMEM accesses are the warp's)
           const float mn = fmaxf(m, top);
           if (m != -INFINITY) l *= ex2(m - mn);
           m = mn;
           float bm = -INFINITY;
 #pragma unroll
-          for (int t = 0; t < 32; ++t) bm = fmaxf(bm, x[t] + (float)((__float_as_int(vfac[t]) >> 23) - 127));
+          for (int t = 0; t < 32; ++t) bm = fmaxf(bm, x[t] + (float)((__float_as_int(T.vfac[t]) >> 23) - 127));
           const float Mn = fmaxf(M, bm - kWeightExp);
           const float back = M == -INFINITY ? 0.f : ex2(M - Mn);
           M = Mn;
           rs = Mn == -INFINITY ? 0.f : ex2(mn - Mn);
-          if (!first) {
+          if (it > 0) {
+            ok &= wait2(I.sums, i - 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tmem_after();
 #pragma unroll 1
-            for (int b = 0; b < NB; ++b) {
-              float o[32];
-              tmem_ld32(mine + R::kO + 32 * b, o);
+            for (int b = 0; b < NB * 2; ++b) {
+              float o[16];
+              tmem_ld16(mine + R::kO + 16 * b, o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= back;
-              tmem_st32(mine + R::kO + 32 * b, o);
+              for (int e = 0; e < 16; ++e) o[e] *= back;
+              uint32_t z[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(o[e]);
+              tmem_st16(mine + R::kO + 16 * b, z);
             }
           }
         }
         // ---- weights
-        {
-          const float mi = m == -INFINITY ? 0.f : m;
-          const float2 r2 = make_float2(rs, rs);
-          float2 sum = make_float2(0.f, 0.f);
-          uint32_t pw[16];
+        const float mi = m == -INFINITY ? 0.f : m;
+        const float2 r2 = make_float2(rs, rs);
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t pw[16];
 #pragma unroll
-          for (int t = 0; t < 32; t += 4) {
-            const float2 y = make_float2(ex2(x[t] - mi), ex2(x[t + 1] - mi));
-            const float2 z = make_float2(ex2(x[t + 2] - mi), ex2(x[t + 3] - mi));
-            sum = add2(sum, add2(y, z));
-            const float4 sc = *reinterpret_cast<const float4*>(vfac + t);
-            const float2 wy = mul2(mul2(y, make_float2(sc.x, sc.y)), r2), wz = mul2(mul2(z, make_float2(sc.z, sc.w)), r2);
-            pw[t / 2] = pack_f16(wy.x, wy.y);
-            pw[t / 2 + 1] = pack_f16(wz.x, wz.y);
-          }
-          l += sum.x + sum.y;
-          __syncwarp();
-          tmem_st16(mine + R::kP, pw);
+        for (int t = 0; t < 32; t += 4) {
+          const float2 y = make_float2(ex2(x[t] - mi), ex2(x[t + 1] - mi));
+          const float2 z = make_float2(ex2(x[t + 2] - mi), ex2(x[t + 3] - mi));
+          sum = add2(sum, add2(y, z));
+          const float4 sc = *reinterpret_cast<const float4*>(T.vfac + t);
+          const float2 wy = mul2(mul2(y, make_float2(sc.x, sc.y)), r2), wz = mul2(mul2(z, make_float2(sc.z, sc.w)), r2);
+          pw[t / 2] = pack_f16(wy.x, wy.y);
+          pw[t / 2 + 1] = pack_f16(wz.x, wz.y);
         }
+        l += sum.x + sum.y;
+        if (i >= 2) ok &= wait2(I.sums, i - 2);   // P of tile i - 2 has been read
+        __syncwarp();
+        tmem_after();
+        tmem_st16(mine + R::kP + 16 * (i & 1), pw);
         tmem_wait_st();
-        fence_proxy_async();
         tmem_before();
-        if (__syncthreads_or(lost)) {
-          lost = true;
-          break;
-        }
-        if (tid == 0) {
-          tmem_after();
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            umma_ts(tmem + R::kO, tmem + R::kP + 8 * k,
-                    smem_desc(smem_u32(sm + R::kV) + k * 2 * R::kVLbo, R::kVLbo, R::kVSbo), idesc(D), !(first && k == 0));
-          umma_commit(smem_u32(bar_o));
-        }
-        busy_o = true;
-        first = false;
-      } else if (__syncthreads_or(lost)) {
-        lost = true;
-        break;
+        mbar_arrive(smem_u32(&I.weights[i & 1]));
       }
-      if (issued < count) issue(slot);   // all threads have read the slot
-      ++done;
-      if (++slot == S) {
-        slot = 0;
-        phase ^= 1;
-      }
-    }
-    if (lost) break;
+      if (!ok) break;
+      done += n_tiles;
 
-    // ------------------------------------------------ the unit's rows, or this block's part of them
-    if (busy_o) {
-      lost |= !mbar_wait_bounded(smem_u32(bar_o), phase_o);
-      phase_o ^= 1;
-      busy_o = false;
-    }
-    if (__syncthreads_or(lost)) {
-      lost = true;
-      break;
-    }
-    tmem_after();
-    const bool whole = first_tile == 0 && n_tiles == cc.tiles;
-    float* part = p.partials + ((size_t)(2 * wid + (first_tile == 0)) * CHUNK + tid) * (D + 4);
-    const int64_t at = (int64_t)(rq.row0 + rho / p.G) * p.Hq + h * p.G + rho % p.G;
-    if (there) {
-      if (!whole) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
-      else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    }
-    const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      // ---------------------------------------------- the unit's rows, or this block's part of them
+      ok &= wait2(I.sums, done - 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tmem_after();
+      const bool whole = first_tile == 0 && n_tiles == cc.tiles;
+      float* part = p.partials + ((size_t)(2 * wid + (first_tile == 0)) * CHUNK + tid) * (D + 4);
+      const int64_t at = (int64_t)(rq.row0 + rho / p.G) * p.Hq + h * p.G + rho % p.G;
+      if (there) {
+        if (!whole) *reinterpret_cast<float2*>(part + D) = make_float2(m, l);
+        else if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      }
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll 1
+      for (int b = 0; b < NB * 2; ++b) {
+        float o[16];
+        __syncwarp();
+        tmem_ld16(mine + R::kO + 16 * b, o);
+        // a row that saw only NaN has no M: its l is NaN
+        const float fb = poison >> (b >> 1) & 1 ? NAN : M == -INFINITY ? l : ex2(M - m) * inv;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float o[32];
-      tmem_ld32(mine + R::kO + 32 * b, o);
-      // a row that saw only NaN has no M: its l is NaN
-      const float fb = poison >> b & 1 ? NAN : M == -INFINITY ? l : ex2(M - m) * inv;
+        for (int e = 0; e < 16; ++e) o[e] *= fb;
+        if (there && !whole) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) o[i] = first ? 0.f : o[i] * fb;
-      if (there && !whole) {
+          for (int e = 0; e < 16; e += 4)
+            *reinterpret_cast<float4*>(part + 16 * b + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        } else if (there) {
+          uint32_t z[8];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4)
-          *reinterpret_cast<float4*>(part + 32 * b + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-      } else if (there) {
-        uint32_t z[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-          z[i] = *reinterpret_cast<const uint32_t*>(&v);
+          for (int e = 0; e < 8; ++e) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+            z[e] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at * D + 16 * b);
+          dst[0] = make_uint4(z[0], z[1], z[2], z[3]);
+          dst[1] = make_uint4(z[4], z[5], z[6], z[7]);
         }
-        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at * D + 32 * b);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = make_uint4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]);
       }
       __syncwarp();
+      if (first_tile == 0 && !whole && tid == 0) {
+        // the blocks after this one that hold the unit's other tiles
+        const int64_t last = begin + done - n_tiles + cc.tiles - 1, longer = (int64_t)extra * (share + 1);
+        const int64_t owner = last < longer ? last / (share + 1) : extra + (last - longer) / share;
+        p.headers[wid] = make_int4((int)(owner - wid), rq.row0, h, rho0 << 8 | rows);
+      }
+      tmem_before();   // the next unit's first weights, and with them its first product, come after this
+      if (done < count) mx_next_unit<CHUNK>(p, &cc);
     }
-    if (first_tile == 0 && !whole && tid == 0) {
-      // the blocks after this one that hold the unit's other tiles
-      const int64_t last = begin + done - n_tiles + cc.tiles - 1, longer = (int64_t)extra * (share + 1);
-      const int64_t owner = last < longer ? last / (share + 1) : extra + (last - longer) / share;
-      p.headers[wid] = make_int4((int)(owner - wid), rq.row0, h, rho0 << 8 | rows);
-    }
-    tmem_before();   // O is read before the next unit's product writes it: the next barrier orders them
-    if (done < count) mx_next_unit<CHUNK>(p, &cc);
+    if (!ok && lane == 0) set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
   }
-  if (lost) {   // copies and products that are still on their way end before the block does
-    if (tid == 0) {
-      set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
-      if (busy_s) mbar_wait_bounded(smem_u32(bar_s), phase_s);
-      if (busy_o) mbar_wait_bounded(smem_u32(bar_o), phase_o);
-      for (int i = done; i < issued; ++i) mbar_wait_bounded(smem_u32(full + i % S), (uint32_t)(i / S) & 1);
+  // products that were issued have ended: the sums of the last one are waited for above
+  if (!ok) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_wait_bounded(smem_u32(&I.scores[i]), 0);
+      mbar_wait_bounded(smem_u32(&I.scores[i]), 1);
     }
   }
   tmem_before();
