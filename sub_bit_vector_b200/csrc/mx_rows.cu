@@ -6,7 +6,7 @@
 // a chunk is 128 rows = the 128 lanes of the accumulators, one thread per row,
 // so that a row's softmax needs no exchange.  Per tile of 32 tokens:
 //   K' (fp16, shared memory) = code * 2^(e - E), E the token's largest scale
-//     exponent; S[128 x 32] = Q K'^T (TMEM), x = S 2^E * scale in fp32.
+//     exponent; S[128 x 32] = Q K'^T (Q and S in TMEM), x = S 2^E * scale in fp32.
 //   P (fp16, TMEM) = 2^(x + E - M), E the largest exponent of the token's value,
 //     M a reference per row, raised as in mx_attn.cu; V' = code * 2^(e - E);
 //     O[128 x D] += P V'.
@@ -14,8 +14,8 @@
 // an element is rounded to 2^-24 of 2^E, which is less than 2^-26 of its token's
 // largest element.  A block of NaN counts as 0 in V' and is put into the outputs
 // of the rows that see it at the end.
-// Four warps convert codes and issue copies and products, four compute the
-// softmax; operands, scores and weights are double-buffered, so that tile i's
+// Four warps convert codes, and one thread each of three of them issues the
+// scores' product, the copies and the product P V; four compute the softmax; operands, scores and weights are double-buffered, so that tile i's
 // softmax, tile i + 1's scores and the product P V of tile i - 1 run together.
 //
 // Operands in shared memory are K-major without swizzle: core matrices of 8
@@ -34,17 +34,16 @@ struct Rows {
   using Tile = MxTile<D, FMT>;
   static constexpr int NB = Tile::kBlocks;
   static constexpr int kStages = 3;
-  static constexpr int kQLbo = 128, kQSbo = D / 8 * 128;                 // rows x channels
   static constexpr int kKLbo = 160, kKSbo = D / 8 * 160;                 // tokens x channels
   static constexpr int kVLbo = 144, kVSbo = 672, kVBlock = 4 * kVSbo;    // channels x tokens, per block
   static constexpr int kKBuf = kMxTile / 8 * kKSbo, kVBuf = NB * kVBlock;
-  static constexpr int kQ = 0, kK = kQ + kMxRowsChunk / 8 * kQSbo, kV = kK + 2 * kKBuf, kRing = kV + 2 * kVBuf,
+  static constexpr int kK = 0, kV = kK + 2 * kKBuf, kRing = kV + 2 * kVBuf,
                        kSlot = 2 * Tile::kBytes, kInfo = kRing + kStages * kSlot;
   static constexpr int kNeed = kInfo + 1024;
   static constexpr int kBytes = kNeed > 76 * 1024 ? kNeed : 76 * 1024;   // two blocks per SM, no third that would wait for TMEM
-  // TMEM columns: O, S twice, P twice
-  static constexpr int kO = 0, kS = D, kP = D + 2 * kMxTile, kCols = 256;
-  static_assert(kP + 32 <= kCols, "TMEM");
+  // TMEM columns: O, Q (two fp16 per column), and twice S, over which P is written
+  static constexpr int kO = 0, kQ = D, kS = D + D / 2, kCols = 256;
+  static_assert(kS + 2 * kMxTile <= kCols, "TMEM");
 };
 // What the converting warps tell the others: per tile in turn, and barriers.
 struct RowsInfo {
@@ -69,12 +68,6 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
 // kind::f16, fp16 operands, K-major, fp32 sums, M = 128
 constexpr uint32_t idesc(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kMxRowsChunk >> 4) << 24);
-}
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
-      : "memory");
 }
 __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {   // A in TMEM
   asm volatile(
@@ -192,21 +185,20 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
   if (warp >= 4) {
     // ======================== conversion, copies, products
     const int w4 = warp - 4;
-    const bool leader = threadIdx.x == 128;
+    const bool leader = threadIdx.x == 128, copier = threadIdx.x == 160, adder = threadIdx.x == 192;   // issue S, copies, P V
     const int sub = w4 >> 1;
     constexpr int UB = NB / 2;   // blocks of a warp, of one half of the tile
     const int b0 = (w4 & 1) * UB;
-    MxCursor pc = cc;            // the leader's: the next tile to copy
+    MxCursor pc = cc;            // the copier's: the next tile
     const int per = p.L.page_tokens / kMxTile;
     int page = pc.t / per, in_page = pc.t % per, issued = 0;
     int64_t head = 0;
     int id = 0;
-    if (leader) {
+    if (copier) {
       head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
       id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
     }
-    auto issue = [&]() {   // by the leader
-      const int slot = issued % S;
+    auto issue = [&](int slot) {   // by the copier
       const uint32_t bar = smem_u32(&I.full[slot]), dst = smem_u32(sm + R::kRing + slot * R::kSlot);
       if (id >= 0 && id < p.L.n_pages) {
         const int64_t at = (head + (int64_t)id * per + in_page) * Tile::kBytes;
@@ -231,8 +223,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         }
       }
     };
-    if (leader)
-      for (int i = 0; i < S && i < count; ++i) issue();
+    if (copier)
+      for (int i = 0; i < S && i < count; ++i) issue(i);
+    int slot = 0;
+    uint32_t phase = 0;
     // Barrier of these warps; false, in all threads alike, once a wait has run out in any.
     auto sync4 = [&]() {
       uint32_t failed;
@@ -248,11 +242,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
     // O += P V of tile i, once its weights are there
     auto product = [&](int i, bool fresh) {
       ok &= wait2(I.weights, i);
-      if (leader) {
+      if (adder) {
         tmem_after();
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          umma_ts(tmem + R::kO, tmem + R::kP + 16 * (i & 1) + 8 * k,
+          umma_ts(tmem + R::kO, tmem + R::kS + kMxTile * (i & 1) + 8 * k,
                   smem_desc(smem_u32(sm + R::kV) + (i & 1) * R::kVBuf + k * 2 * R::kVLbo, R::kVLbo, R::kVSbo), idesc(D),
                   !(fresh && k == 0));
         umma_commit(smem_u32(&I.sums[i & 1]));
@@ -264,13 +258,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
       const int first_tile = cc.t, n_tiles = min(cc.tiles - cc.t, count - done);
       const uint64_t all_new = rq.n >= 64 ? ~0ull : (1ull << rq.n) - 1;
       for (int it = 0; it < n_tiles; ++it) {
-        const int i = done, slot = i % S;
+        const int i = done;
         auto& T = I.t[i & 1];
         const int tok0 = (first_tile + it) * kMxTile;
         const bool edge = tok0 + kMxTile > rq.base;
-        ok &= mbar_wait_bounded(smem_u32(&I.full[slot]), (uint32_t)(i / S) & 1);
+        ok &= mbar_wait_bounded(smem_u32(&I.full[slot]), phase);
         const bool bad = *reinterpret_cast<volatile uint32_t*>(&I.bad) >> slot & 1;
-        if (i >= 2) ok &= wait2(I.scores, i - 2);   // K' of tile i - 2 has been read
+        // (K' of tile i - 2 has been read: its weights were waited for)
         const uint8_t* const sk = sm + R::kRing + slot * R::kSlot;
         const uint8_t* const sv = sk + Tile::kBytes;
         uint32_t w[UB][4];   // e4m3: 4 words of a block; e2m1: 2
@@ -358,10 +352,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         if (!(go = sync4())) break;
         if (leader) {
           if (it == 0) ok &= mbar_wait_bounded(smem_u32(&I.query), (uint32_t)units & 1);
+          if (i >= 2) ok &= wait2(I.sums, i - 2);   // P of tile i - 2, where S goes, has been read
           tmem_after();
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            umma_ss(tmem + R::kS + (i & 1) * kMxTile, smem_desc(smem_u32(sm + R::kQ) + k * 2 * R::kQLbo, R::kQLbo, R::kQSbo),
+            umma_ts(tmem + R::kS + (i & 1) * kMxTile, tmem + R::kQ + 8 * k,
                     smem_desc(smem_u32(dk) + k * 2 * R::kKLbo, R::kKLbo, R::kKSbo), idesc(kMxTile), k > 0);
           umma_commit(smem_u32(&I.scores[i & 1]));
         }
@@ -394,9 +389,13 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         }
         fence_proxy_async();
         if (!(go = sync4())) break;   // the raw tile has been read, V' is written
-        if (leader) {
+        if (copier) {
           if (bad) atomicAnd(&I.bad, ~(1u << slot));
-          if (issued < count) issue();
+          if (issued < count) issue(slot);
+        }
+        if (++slot == S) {
+          slot = 0;
+          phase ^= 1;
         }
         if (it > 0) product(i - 1, it == 1);
         if (it == n_tiles - 1) product(i, it == 0);
@@ -406,7 +405,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
       if (done < count && go) mx_next_unit<CHUNK>(p, &cc);
     }
     if (!ok && lane == 0) set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
-    if (leader && !ok)   // copies that are still on their way end before the block does
+    if (copier && !ok)   // copies that are still on their way end before the block does
       for (int i = max(0, issued - S); i < issued; ++i) mbar_wait_bounded(smem_u32(&I.full[i % S]), (uint32_t)(i / S) & 1);
   } else {
     // ======================== softmax: a thread has a row
@@ -458,15 +457,16 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
         f = p.softcap > 0.f ? p.scale / p.softcap * down : p.scale * kLog2e * down;
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          uint32_t z[4];
+        for (int k = 0; k < D / 32; ++k) {
+          uint32_t z[16];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) z[j] = pack_f16(bf16_lo(q[4 * k + j]) * up, bf16_hi(q[4 * k + j]) * up);
-          *reinterpret_cast<uint4*>(sm + R::kQ + (tid >> 3) * R::kQSbo + k * R::kQLbo + (tid & 7) * 16) =
-              make_uint4(z[0], z[1], z[2], z[3]);
+          for (int j = 0; j < 16; ++j) z[j] = pack_f16(bf16_lo(q[16 * k + j]) * up, bf16_hi(q[16 * k + j]) * up);
+          __syncwarp();
+          tmem_st16(mine + R::kQ + 16 * k, z);
         }
       }
-      fence_proxy_async();
+      tmem_wait_st();
+      tmem_before();
       mbar_arrive(smem_u32(&I.query));
 
       float m = -INFINITY, l = 0.f, M = -INFINITY, rs = 0.f;
@@ -556,13 +556,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         }
         // ---- weights
         const float mi = m == -INFINITY ? 0.f : m;
-        const float2 r2 = make_float2(rs, rs);
+        const float2 r2 = make_float2(rs, rs), n2 = make_float2(-mi, -mi);
         float2 sum = make_float2(0.f, 0.f);
         uint32_t pw[16];
 #pragma unroll
         for (int t = 0; t < 32; t += 4) {
-          const float2 y = make_float2(ex2(x[t] - mi), ex2(x[t + 1] - mi));
-          const float2 z = make_float2(ex2(x[t + 2] - mi), ex2(x[t + 3] - mi));
+          float2 y = add2(make_float2(x[t], x[t + 1]), n2), z = add2(make_float2(x[t + 2], x[t + 3]), n2);
+          y = make_float2(ex2(y.x), ex2(y.y));
+          z = make_float2(ex2(z.x), ex2(z.y));
           sum = add2(sum, add2(y, z));
           const float4 sc = *reinterpret_cast<const float4*>(T.vfac + t);
           const float2 wy = mul2(mul2(y, make_float2(sc.x, sc.y)), r2), wz = mul2(mul2(z, make_float2(sc.z, sc.w)), r2);
@@ -570,10 +571,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
           pw[t / 2 + 1] = pack_f16(wz.x, wz.y);
         }
         l += sum.x + sum.y;
-        if (i >= 2) ok &= wait2(I.sums, i - 2);   // P of tile i - 2 has been read
         __syncwarp();
-        tmem_after();
-        tmem_st16(mine + R::kP + 16 * (i & 1), pw);
+        tmem_st16(mine + R::kS + kMxTile * (i & 1), pw);   // S has been read; P of tile i - 2 was, before S was written
         tmem_wait_st();
         tmem_before();
         mbar_arrive(smem_u32(&I.weights[i & 1]));
