@@ -14,8 +14,8 @@
 // an element is rounded to 2^-24 of 2^E, which is less than 2^-26 of its token's
 // largest element.  A block of NaN counts as 0 in V' and is put into the outputs
 // of the rows that see it at the end.
-// Four warps convert codes, and one thread each of three of them issues the
-// scores' product, the copies and the product P V; four compute the softmax; operands, scores and weights are double-buffered, so that tile i's
+// Four warps convert codes, and two of them issue the products; four compute the softmax (and one
+// thread of them issues the copies); operands, scores and weights are double-buffered, so that tile i's
 // softmax, tile i + 1's scores and the product P V of tile i - 1 run together.
 //
 // Operands in shared memory are K-major without swizzle: core matrices of 8
@@ -33,7 +33,7 @@ template <int D, int FMT>
 struct Rows {
   using Tile = MxTile<D, FMT>;
   static constexpr int NB = Tile::kBlocks;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = 4;
   static constexpr int kKLbo = 160, kKSbo = D / 8 * 160;                 // tokens x channels
   static constexpr int kVLbo = 144, kVSbo = 672, kVBlock = 4 * kVSbo;    // channels x tokens, per block
   static constexpr int kKBuf = kMxTile / 8 * kKSbo, kVBuf = NB * kVBlock;
@@ -51,11 +51,11 @@ struct RowsInfo {
     float fac[kMxTile];    // 2^E of each key
     float vfac[kMxTile];   // of each value, NaN left out
     int pos[kMxTile];      // positions (with slopes)
-    uint32_t nan[4];       // [block]: tokens whose value is NaN there
-    float vmax;            // largest of vfac
+    uint8_t nan[4][4];     // [block][quarter]: tokens whose value is NaN there
+    float vmax[4];         // largest of vfac in each quarter
     uint32_t hidden;       // the page is not in the pool
   } t[2];
-  uint64_t full[4];                               // raw tiles
+  uint64_t full[4], freed[4];                     // raw tiles: arrived, read
   uint64_t told[2], scores[2], weights[2], sums[2];   // info written; S, P, O += P V done
   uint64_t query;                                 // Q written
   uint32_t tmem, bad;
@@ -69,14 +69,27 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
 constexpr uint32_t idesc(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kMxRowsChunk >> 4) << 24);
 }
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {   // A in TMEM
+// Issued by a whole warp with the same arguments, of which the elected thread
+// acts: the arguments then stay in uniform registers, without which the eight
+// instructions of a score tile took 1000 cycles to issue.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc, uint32_t e) {   // A in TMEM
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc), "r"(e)
       : "memory");
 }
-__device__ __forceinline__ void umma_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void umma_commit(uint32_t bar, uint32_t e) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(e)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -161,8 +174,11 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&I.tmem)), "r"(R::kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  if (threadIdx.x == 128) {
-    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&I.full[i]), 1);
+  if (threadIdx.x == 160) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(smem_u32(&I.full[i]), 1);
+      mbar_init(smem_u32(&I.freed[i]), 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&I.told[i]), 4);
       mbar_init(smem_u32(&I.scores[i]), 1);
@@ -184,47 +200,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
 
   if (warp >= 4) {
     // ======================== conversion, copies, products
-    const int w4 = warp - 4;
-    const bool leader = threadIdx.x == 128, copier = threadIdx.x == 160, adder = threadIdx.x == 192;   // issue S, copies, P V
+    const int w4 = __shfl_sync(0xffffffffu, warp - 4, 0);
+    const bool leader = w4 == 0, adder = w4 == 2;   // these warps issue S and P V
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t desc_k = smem_desc(smem_u32(sm + R::kK), R::kKLbo, R::kKSbo);
+    const uint64_t desc_v = smem_desc(smem_u32(sm + R::kV), R::kVLbo, R::kVSbo);
     const int sub = w4 >> 1;
     constexpr int UB = NB / 2;   // blocks of a warp, of one half of the tile
     const int b0 = (w4 & 1) * UB;
-    MxCursor pc = cc;            // the copier's: the next tile
-    const int per = p.L.page_tokens / kMxTile;
-    int page = pc.t / per, in_page = pc.t % per, issued = 0;
-    int64_t head = 0;
-    int id = 0;
-    if (copier) {
-      head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
-      id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
-    }
-    auto issue = [&](int slot) {   // by the copier
-      const uint32_t bar = smem_u32(&I.full[slot]), dst = smem_u32(sm + R::kRing + slot * R::kSlot);
-      if (id >= 0 && id < p.L.n_pages) {
-        const int64_t at = (head + (int64_t)id * per + in_page) * Tile::kBytes;
-        mbar_arrive_expect_tx(bar, 2 * Tile::kBytes);
-        bulk_g2s(dst, p.pk + at, Tile::kBytes, bar);
-        bulk_g2s(dst + Tile::kBytes, p.pv + at, Tile::kBytes, bar);
-      } else {
-        set_fault(p.fault, LOOPVQ_FAULT_POOL_RANGE);
-        atomicOr(&I.bad, 1u << slot);   // before the arrival that publishes it
-        mbar_arrive(bar);
-      }
-      if (++issued < count) {
-        if (++pc.t == pc.tiles) {
-          mx_next_unit<CHUNK>(p, &pc);
-          page = in_page = 0;
-          head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
-          id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages);
-        } else if (++in_page == per) {
-          in_page = 0;
-          ++page;
-          id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
-        }
-      }
-    };
-    if (copier)
-      for (int i = 0; i < S && i < count; ++i) issue(i);
     int slot = 0;
     uint32_t phase = 0;
     // Barrier of these warps; false, in all threads alike, once a wait has run out in any.
@@ -243,13 +226,14 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
     auto product = [&](int i, bool fresh) {
       ok &= wait2(I.weights, i);
       if (adder) {
+        __syncwarp();
         tmem_after();
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          umma_ts(tmem + R::kO, tmem + R::kS + kMxTile * (i & 1) + 8 * k,
-                  smem_desc(smem_u32(sm + R::kV) + (i & 1) * R::kVBuf + k * 2 * R::kVLbo, R::kVLbo, R::kVSbo), idesc(D),
-                  !(fresh && k == 0));
-        umma_commit(smem_u32(&I.sums[i & 1]));
+        const uint32_t el = elect();
+        const uint64_t dv = desc_v + (uint64_t)(i & 1) * (R::kVBuf >> 4);
+        const uint32_t pa = tm + R::kS + kMxTile * (i & 1);
+        umma_ts(tm + R::kO, pa, dv, idesc(D), !fresh, el);
+        umma_ts(tm + R::kO, pa + 8, dv + (2 * R::kVLbo >> 4), idesc(D), 1, el);
+        umma_commit(smem_u32(&I.sums[i & 1]), el);
       }
     };
     while (done < count && go) {
@@ -267,8 +251,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         // (K' of tile i - 2 has been read: its weights were waited for)
         const uint8_t* const sk = sm + R::kRing + slot * R::kSlot;
         const uint8_t* const sv = sk + Tile::kBytes;
-        uint32_t w[UB][4];   // e4m3: 4 words of a block; e2m1: 2
-        auto load_codes = [&](const uint8_t* tile) {
+        uint32_t w[UB][4], wv[UB][4];   // e4m3: 4 words of a block; e2m1: 2
+        auto load_codes = [&](const uint8_t* tile, uint32_t (&w)[UB][4]) {
 #pragma unroll
           for (int k = 0; k < UB; ++k) {
             if constexpr (FMT == LOOPVQ_MX_E4M3) {
@@ -282,7 +266,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
           }
         };
         // ---- K'
-        load_codes(sk);
+        load_codes(sk, w);
+        load_codes(sv, wv);
         uint32_t scw[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) scw[b] = *reinterpret_cast<const uint32_t*>(sk + mx_scale_off<D, FMT>(sub * 4 + (g >> 1), b));
@@ -312,32 +297,29 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
                 make_uint4(mul_f16(hc[0], s2), mul_f16(hc[1], s2), mul_f16(hc[2], s2), mul_f16(hc[3], s2));
           }
         }
-        if (w4 == 3 && lane < 8) {   // V's factors: a lane has a quad of tokens
-          float top[4] = {0.f, 0.f, 0.f, 0.f};
+        {   // V's factors: a warp has 8 tokens, a lane a block of one
+          const int vt = lane / NB & 7, vb = lane % NB;
+          const uint32_t ve = sv[mx_scale_off<D, FMT>(2 * w4 + (vt >> 2), vb) + (vt & 3)];
+          const bool is_nan = ve == kMxNan;
+          float top = is_nan ? 0.f : __uint_as_float(ve << 23);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const uint32_t z = *reinterpret_cast<const uint32_t*>(sv + mx_scale_off<D, FMT>(lane, b));
-            uint32_t nan = 0;
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const float y = scale_f32(z, t);
-              if (y == INFINITY) nan |= 1u << (4 * lane + t);
-              else top[t] = fmaxf(top[t], y);
+          for (int d = 1; d < NB; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));   // not negative
+          const uint32_t nans = __ballot_sync(0xffffffffu, is_nan);
+          if (vb == 0) T.vfac[8 * w4 + vt] = top;
+          if (lane < NB) {
+            uint32_t z = 0;
+            if (nans) {
+              for (int t = 0; t < 8; ++t) z |= (nans >> (t * NB + lane) & 1u) << t;
             }
-#pragma unroll
-            for (int d = 1; d < 8; d <<= 1) nan |= __shfl_xor_sync(0xffu, nan, d);
-            if (lane == 0) T.nan[b] = nan;
+            T.nan[lane][w4] = (uint8_t)z;
           }
-          *reinterpret_cast<float4*>(T.vfac + 4 * lane) = make_float4(top[0], top[1], top[2], top[3]);
-          float all = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-#pragma unroll
-          for (int d = 1; d < 8; d <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffu, all, d));
           if (lane == 0) {
-            T.vmax = all;
-            T.hidden = bad;
+            T.vmax[w4] = __uint_as_float(most);
+            if (w4 == 0) T.hidden = bad;
           }
         }
-        if (p.slopes && w4 == 1) {
+        if (p.slopes && w4 == 0) {
           const int j = tok0 + lane - rq.base;
           int at = tok0 + lane;
           if (j >= 0 && j < rq.n) {
@@ -353,15 +335,16 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         if (leader) {
           if (it == 0) ok &= mbar_wait_bounded(smem_u32(&I.query), (uint32_t)units & 1);
           if (i >= 2) ok &= wait2(I.sums, i - 2);   // P of tile i - 2, where S goes, has been read
+          __syncwarp();
           tmem_after();
+          const uint32_t el = elect();
+          const uint64_t d = desc_k + (uint64_t)(i & 1) * (R::kKBuf >> 4);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            umma_ts(tmem + R::kS + (i & 1) * kMxTile, tmem + R::kQ + 8 * k,
-                    smem_desc(smem_u32(dk) + k * 2 * R::kKLbo, R::kKLbo, R::kKSbo), idesc(kMxTile), k > 0);
-          umma_commit(smem_u32(&I.scores[i & 1]));
+            umma_ts(tm + R::kS + (i & 1) * kMxTile, tm + R::kQ + 8 * k, d + k * (2 * R::kKLbo >> 4), idesc(kMxTile), k > 0, el);
+          umma_commit(smem_u32(&I.scores[i & 1]), el);
         }
         // ---- V'
-        load_codes(sv);
         const float4 ve = *reinterpret_cast<const float4*>(T.vfac + sub * 16 + 4 * c);   // of this lane's tokens
         if (i >= 2) ok &= wait2(I.sums, i - 2);   // V' of tile i - 2 has been read
         uint8_t* const dv = sm + R::kV + (i & 1) * R::kVBuf;
@@ -370,10 +353,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
           uint32_t hv[4][2];   // [channel j][token pair]
           if constexpr (FMT == LOOPVQ_MX_E4M3) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) codes_e4m3(edge ? drop_nan_codes(w[k][j]) : w[k][j], hv[j]);
+            for (int j = 0; j < 4; ++j) codes_e4m3(edge ? drop_nan_codes(wv[k][j]) : wv[k][j], hv[j]);
           } else {
-            codes_e2m1(w[k][0], hv[0]);
-            codes_e2m1(w[k][1], hv[2]);
+            codes_e2m1(wv[k][0], hv[0]);
+            codes_e2m1(wv[k][1], hv[2]);
           }
           // a NaN block's ratio is large: its codes are 0, and so is what it gives
           const uint32_t z = *reinterpret_cast<const uint32_t*>(sv + mx_scale_off<D, FMT>(sub * 4 + c, b0 + k));
@@ -389,10 +372,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         }
         fence_proxy_async();
         if (!(go = sync4())) break;   // the raw tile has been read, V' is written
-        if (copier) {
-          if (bad) atomicAnd(&I.bad, ~(1u << slot));
-          if (issued < count) issue(slot);
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&I.freed[slot]));
         if (++slot == S) {
           slot = 0;
           phase ^= 1;
@@ -405,12 +385,48 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
       if (done < count && go) mx_next_unit<CHUNK>(p, &cc);
     }
     if (!ok && lane == 0) set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
-    if (copier && !ok)   // copies that are still on their way end before the block does
-      for (int i = max(0, issued - S); i < issued; ++i) mbar_wait_bounded(smem_u32(&I.full[i % S]), (uint32_t)(i / S) & 1);
   } else {
     // ======================== softmax: a thread has a row
     const int tid = threadIdx.x;
     const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);   // this warp's lanes
+    MxCursor pc = cc;            // the copier's: the next tile
+    const int per = p.L.page_tokens / kMxTile;
+    int page = pc.t / per, in_page = pc.t % per, issued = 0;
+    int64_t head = 0;
+    int id = 0;
+    auto issue = [&](int slot) {   // by the copier
+      const uint32_t bar = smem_u32(&I.full[slot]), dst = smem_u32(sm + R::kRing + slot * R::kSlot);
+      if (id >= 0 && id < p.L.n_pages) {
+        const int64_t at = (head + (int64_t)id * per + in_page) * Tile::kBytes;
+        mbar_arrive_expect_tx(bar, 2 * Tile::kBytes);
+        bulk_g2s(dst, p.pk + at, Tile::kBytes, bar);
+        bulk_g2s(dst + Tile::kBytes, p.pv + at, Tile::kBytes, bar);
+      } else {
+        set_fault(p.fault, LOOPVQ_FAULT_POOL_RANGE);
+        atomicOr(&I.bad, 1u << slot);   // before the arrival that publishes it
+        mbar_arrive(bar);
+      }
+      if (++issued < count) {
+        if (++pc.t == pc.tiles) {
+          mx_next_unit<CHUNK>(p, &pc);
+          page = in_page = 0;
+          head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
+          id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages);
+        } else if (++in_page == per) {
+          in_page = 0;
+          ++page;
+          id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+        }
+      }
+    };
+    const bool copier = tid == 96;
+    if (copier) {
+      head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
+      id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+      for (int i = 0; i < S && i < count; ++i) issue(i);
+    }
+    int slot = 0;
+    uint32_t phase = 0;
     while (done < count && ok) {
       MxReq rq = {};
       mx_request(p.L, cc.r, &rq, nullptr);
@@ -524,7 +540,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
 #pragma unroll
         for (int t = 0; t < 32; ++t) top = fmaxf(top, x[t]);
         // ---- raise the references if a score or a weight could leave its range
-        const bool over = top > m + kScoreSlack || ex2(top - (m == -INFINITY ? 0.f : m)) * T.vmax * rs > kWeightMax;
+        const bool over = top > m + kScoreSlack || ex2(top - (m == -INFINITY ? 0.f : m)) * fmaxf(fmaxf(T.vmax[0], T.vmax[1]), fmaxf(T.vmax[2], T.vmax[3])) * rs > kWeightMax;
         if (__any_sync(0xffffffffu, over)) {   // (all lanes: the TMEM accesses are the warp's)
           const float mn = fmaxf(m, top);
           if (m != -INFINITY) l *= ex2(m - mn);
@@ -576,6 +592,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         tmem_wait_st();
         tmem_before();
         mbar_arrive(smem_u32(&I.weights[i & 1]));
+        if (copier) {   // refill the ring where the conversion has read it
+          ok &= mbar_wait_bounded(smem_u32(&I.freed[slot]), phase);
+          if (*reinterpret_cast<volatile uint32_t*>(&I.bad) >> slot & 1) atomicAnd(&I.bad, ~(1u << slot));
+          if (issued < count) issue(slot);
+        }
+        if (++slot == S) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
       if (!ok) break;
       done += n_tiles;
@@ -629,6 +654,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
       if (done < count) mx_next_unit<CHUNK>(p, &cc);
     }
     if (!ok && lane == 0) set_fault(p.fault, LOOPVQ_FAULT_TIMEOUT);
+    if (copier && !ok)   // copies that are still on their way end before the block does
+      for (int i = max(0, issued - S); i < issued; ++i) mbar_wait_bounded(smem_u32(&I.full[i % S]), (uint32_t)(i / S) & 1);
   }
   // products that were issued have ended: the sums of the last one are waited for above
   if (!ok) {
