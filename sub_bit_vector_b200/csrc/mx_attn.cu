@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_rows_kernel(const M
 #pragma unroll
     for (int e = 0; e < kCh; ++e) o[e] *= back;
     const int n = min(32, hd.x + 1 - k0);
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < n; ++k) add_part<kCh>(part(k0 + k), lane, __shfl_sync(0xffffffffu, fl, k), o);
     top = tn;
   }
@@ -780,7 +780,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_rows_kernel(const M
   if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
-constexpr int kRowsFrom = 32;   // more rows than this: mx_rows_kernel
+// More rows than this: mx_rows_kernel.
+template <int D>
+constexpr int kRowsFrom = D == 128 ? 40 : 64;
 // The variant of a call: columns per row, groups.
 struct AttnVariant {
   int narrow, nt, chunk;
@@ -800,7 +802,7 @@ AttnVariant attn_variant_t(int64_t rows, bool fine) {
            : v.narrow    ? (v.nt == 2 ? MxRing<D, FMT, 1, 2>::kWarps : MxRing<D, FMT, 1, 1>::kWarps)
                          : (v.nt == 2 ? MxRing<D, FMT, 0, 2>::kWarps : MxRing<D, FMT, 0, 1>::kWarps);
   v.workers = device_sm_count() * v.per_block;
-  v.rows = !fine && rows > kRowsFrom;
+  v.rows = !fine && rows > kRowsFrom<D>;
   if (v.rows) {
     v.chunk = kMxRowsChunk;
     v.workers = mx_rows_workers();
@@ -827,12 +829,17 @@ int attn_grid(const loopvq_mx_desc* d, const loopvq_mx_layout* l, const AttnVari
   return n < 1 ? 1 : n < most ? (int)n : most;
 }
 
+// How many parts a unit has is known on the device only; with full lengths it is
+// workers / units.  From 24 on a block per row (8 rows of 16 heads over 32K, 100
+// parts: 45.5 us in all against 59), below that a warp per row.
 template <int D, int CHUNK>
 loopvq_status launch_merge(const MxAttnParams& p, int64_t rows, cudaStream_t s) {
+  const int64_t units = (int64_t)p.L.batch * p.H * ((rows + CHUNK - 1) / CHUNK);
+  const bool many_parts = p.n_workers > 24 * units;
   cudaLaunchConfig_t cfg = {};
   const int most = (int)(rows < CHUNK ? rows : CHUNK);
-  cfg.gridDim = CHUNK < 8 ? dim3((p.n_workers + kMergeHeads - 1) / kMergeHeads, most)
-                          : dim3(p.n_workers, (most + kMergeWarps - 1) / kMergeWarps);
+  cfg.gridDim = many_parts ? dim3((p.n_workers + kMergeHeads - 1) / kMergeHeads, most < 16 ? most : 16)
+                           : dim3(p.n_workers, (most + kMergeWarps - 1) / kMergeWarps);
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -840,9 +847,8 @@ loopvq_status launch_merge(const MxAttnParams& p, int64_t rows, cudaStream_t s) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e;
-  if constexpr (CHUNK < 8) e = cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, CHUNK>, p);
-  else e = cudaLaunchKernelEx(&cfg, mx_merge_rows_kernel<D, CHUNK>, p);
+  const cudaError_t e = many_parts ? cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, CHUNK>, p)
+                                   : cudaLaunchKernelEx(&cfg, mx_merge_rows_kernel<D, CHUNK>, p);
   return e == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }
 template <int D, int FMT, int NARROW, int TERMS, int NT>
