@@ -118,6 +118,76 @@ __device__ __forceinline__ void store_channels(T* p, const float* v) {
   }
 }
 
+// N consecutive channels as they are in memory: two bf16 or one fp32 a word.
+template <typename T, int N, bool VEC>
+struct MxRaw {
+  static constexpr int kWords = N * (int)sizeof(T) / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (!VEC) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(T) == 2) {
+          const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + 2 * i;
+          w[i] = (uint32_t)q[0] | (uint32_t)q[1] << 16;
+        } else {
+          w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        }
+      }
+    } else if constexpr (kWords == 2) {
+      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+      w[0] = u.x; w[1] = u.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // Largest magnitude's bits: 16 of bf16 (compared in pairs), 32 of fp32.
+  __device__ __forceinline__ uint32_t peak() const {
+    uint32_t m = 0;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+      return max(m & 0xffffu, m >> 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) m = max(m, w[i] & 0x7fffffffu);
+      return m;
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 2) return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+    else return __uint_as_float(w[i]);
+  }
+};
+// The peaks of CNT blocks over the lanes that differ in the bits FROM .. TO of
+// their number, as fp32 bits.  bf16 peaks travel in pairs.
+template <typename T, int CNT, int FROM, int TO>
+__device__ __forceinline__ void mx_peaks(uint32_t (&m)[CNT]) {
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int i = 0; i < CNT; i += 2) {
+      uint32_t w = m[i] | m[i + 1] << 16;
+#pragma unroll
+      for (int d = FROM; d <= TO; d <<= 1) w = __vmaxu2(w, __shfl_xor_sync(0xffffffffu, w, d));
+      m[i] = w << 16;
+      m[i + 1] = w & 0xffff0000u;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i)
+#pragma unroll
+      for (int d = FROM; d <= TO; d <<= 1) m[i] = max(m[i], __shfl_xor_sync(0xffffffffu, m[i], d));
+  }
+}
+
 // What a warp of the write and read kernels works on.
 struct MxUnit {
   MxReq q;
@@ -164,36 +234,34 @@ __global__ void __launch_bounds__(256, 3) mx_write_kernel(const MxMoveParams p) 
     if (u.kind == LOOPVQ_KEYS) {
       const int tok[2] = {first + 4 * (g >> 1) + (g & 1), first + 4 * (g >> 1) + (g & 1) + 2};
       const bool in[2] = {tok[0] >= u.q.base && tok[0] < u.q.ctx, tok[1] >= u.q.base && tok[1] < u.q.ctx};
-      float v[2][NB][8];
+      MxRaw<T, 8, VEC> v[2][NB];
 #pragma unroll
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          if (in[a])
-            load_channels<T, 8, VEC>(x + (int64_t)(tok[a] - u.q.base) * p.sn + 32 * b + 8 * c, v[a][b]);
-          else
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[a][b][i] = 0.f;
+          if (in[a]) v[a][b].load(x + (int64_t)(tok[a] - u.q.base) * p.sn + 32 * b + 8 * c);
+          else v[a][b].zero();
         }
       uint32_t sc[2] = {0, 0}, lo[2][NB], hi[2][NB];
 #pragma unroll
-      for (int a = 0; a < 2; ++a)
+      for (int a = 0; a < 2; ++a) {
+        uint32_t m[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) m[b] = v[a][b].peak();
+        mx_peaks<T, NB, 1, 2>(m);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[a][b][i]));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
           float inv;
-          const uint32_t byte = mx_scale<FMT>(m, &inv);
+          const uint32_t byte = mx_scale<FMT>(m[b], &inv);
           sc[a] |= byte << (8 * b);
-          float* w = v[a][b];
-          const bool fin = byte != kMxNan;
-          lo[a][b] = fin ? mx_codes4<FMT>(w[0] * inv, w[1] * inv, w[2] * inv, w[3] * inv) : 0u;
-          hi[a][b] = fin ? mx_codes4<FMT>(w[4] * inv, w[5] * inv, w[6] * inv, w[7] * inv) : 0u;
+          const auto& w = v[a][b];
+          const uint32_t keep = byte != kMxNan ? ~0u : 0u;
+          lo[a][b] = mx_codes4<FMT>(w[0] * inv, w[1] * inv, w[2] * inv, w[3] * inv);
+          hi[a][b] = mx_codes4<FMT>(w[4] * inv, w[5] * inv, w[6] * inv, w[7] * inv) & keep;
           if constexpr (FMT == LOOPVQ_MX_E2M1) lo[a][b] |= hi[a][b] << 16;
+          lo[a][b] &= keep;
         }
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint8_t* d = u.tile + mx_code_off<D, FMT>(sub, b, lane);
@@ -224,40 +292,34 @@ __global__ void __launch_bounds__(256, 3) mx_write_kernel(const MxMoveParams p) 
     } else {
       const int tok = first + 4 * c;
       uint32_t in_mask = 0;   // a byte per new token of the quad
-      float v[4][NB][4];
+      MxRaw<T, 4, VEC> v[4][NB];
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const bool in = tok + t >= u.q.base && tok + t < u.q.ctx;
         in_mask |= in ? 0xffu << (8 * t) : 0u;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          if (in)
-            load_channels<T, 4, VEC>(x + (int64_t)(tok + t - u.q.base) * p.sn + 32 * b + 4 * g, v[t][b]);
-          else
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[t][b][i] = 0.f;
+          if (in) v[t][b].load(x + (int64_t)(tok + t - u.q.base) * p.sn + 32 * b + 4 * g);
+          else v[t][b].zero();
         }
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        uint32_t sc = 0;
+        uint32_t m[4], sc = 0, keep = 0;
+        float inv[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) m[t] = v[t][b].peak();
+        mx_peaks<T, 4, 4, 16>(m);
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m = max(m, abs_bits(v[t][b][i]));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 4));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 8));
-          m = max(m, __shfl_xor_sync(0xffffffffu, m, 16));
-          float inv;
-          const uint32_t byte = mx_scale<FMT>(m, &inv);
+          const uint32_t byte = mx_scale<FMT>(m[t], &inv[t]);
           sc |= byte << (8 * t);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[t][b][i] = byte != kMxNan ? v[t][b][i] * inv : 0.f;
+          keep |= byte == kMxNan ? 0u : (FMT == LOOPVQ_MX_E4M3 ? 0xffu << (8 * t) : 0xfu << (4 * t));
         }
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = mx_codes4<FMT>(v[0][b][j], v[1][b][j], v[2][b][j], v[3][b][j]);
+        for (int j = 0; j < 4; ++j)
+          w[j] = mx_codes4<FMT>(v[0][b][j] * inv[0], v[1][b][j] * inv[1], v[2][b][j] * inv[2], v[3][b][j] * inv[3]) & keep;
         uint8_t* d = u.tile + mx_code_off<D, FMT>(sub, b, lane);
         uint32_t* ds = reinterpret_cast<uint32_t*>(u.tile + mx_scale_off<D, FMT>(sub * 4 + c, b));
         if (in_mask == 0) continue;
