@@ -30,8 +30,6 @@ struct MxMoveParams {
   uint32_t* fault;
 };
 
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
 // Scale byte of a block with largest magnitude bits m, and 2^-e.
 template <int FMT>
 __device__ __forceinline__ uint32_t mx_scale(uint32_t m, float* inv) {
@@ -61,34 +59,7 @@ __device__ __forceinline__ uint32_t mx_codes4(float a, float b, float c, float d
   }
 }
 
-// N consecutive channels of x; vector loads when VEC.
-template <typename T, int N, bool VEC>
-__device__ __forceinline__ void load_channels(const T* p, float* v) {
-  if constexpr (VEC && sizeof(T) == 2) {
-    uint32_t w[N / 2];
-    if constexpr (N == 8) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-    } else {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = u.x; w[1] = u.y;
-    }
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-      v[2 * i] = bf16_lo(w[i]);
-      v[2 * i + 1] = bf16_hi(w[i]);
-    }
-  } else if constexpr (VEC) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(p) + i);
-      v[4 * i] = u.x; v[4 * i + 1] = u.y; v[4 * i + 2] = u.z; v[4 * i + 3] = u.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = to_f32<T>(p[i]);
-  }
-}
+// N consecutive channels; vector stores when VEC.
 template <typename T, int N, bool VEC>
 __device__ __forceinline__ void store_channels(T* p, const float* v) {
   if constexpr (sizeof(T) == 2) {
@@ -219,7 +190,7 @@ __device__ __forceinline__ bool mx_unit(const MxMoveParams& p, MxUnit* u) {
 // Quantise: K lanes hold 8 channels of two tokens per block, V lanes 4
 // channels of four tokens.
 template <int D, int FMT, typename T, bool VEC>
-__global__ void __launch_bounds__(256, 3) mx_write_kernel(const MxMoveParams p) {
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) mx_write_kernel(const MxMoveParams p) {
   using Tile = MxTile<D, FMT>;
   constexpr int NB = Tile::kBlocks;
   MxUnit u;
@@ -450,7 +421,7 @@ __global__ void __launch_bounds__(256) mx_read_kernel(const MxMoveParams p) {
 // for one.  Here a lane holds 4 channels of the tokens of a quad (4 * i ..
 // 4 * i + 3 of a tile): the bytes of a quad that a lane reads or writes are its
 // own, so quads with old tokens are merged in registers without exchange.  A
-// warp covers 128 channels: one head (D = 128) or two (64), of K or of V.
+// warp covers 128 channels: one head (D = 128) or two (64).
 template <int D, int FMT>
 struct MxQuad {
   using Tile = MxTile<D, FMT>;
@@ -511,19 +482,18 @@ struct MxQuad {
   __device__ __forceinline__ uint8_t* scale(int t) const { return tile + mx_scale_off<D, FMT>(sub * 4 + c, b) + t; }
 };
 
-// What a lane of the kernels for a few tokens works on: head and kind.
+// What a lane of the kernels for a few tokens works on: K and V of a head,
+// whose loads are on their way together.
 template <int D>
 struct MxFew {
   MxReq q;
-  int kind, h;
+  int h;
   bool there;
   __device__ __forceinline__ MxFew(const MxLayout& L, int H, uint32_t* fault) {
     constexpr int kHeads = 128 / D;
-    const int groups = (H + kHeads - 1) / kHeads;   // of one kind
     const int w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    kind = w >= groups;
-    h = (w - kind * groups) * kHeads + (threadIdx.x & 31) / (D / 4);
-    there = w < 2 * groups && mx_request(L, blockIdx.z, &q, fault) && q.n > 0;   // uniform in the warp
+    h = w * kHeads + (threadIdx.x & 31) / (D / 4);
+    there = w < (H + kHeads - 1) / kHeads && mx_request(L, blockIdx.z, &q, fault) && q.n > 0;   // uniform in the warp
   }
 };
 
@@ -534,42 +504,43 @@ __global__ void __launch_bounds__(256) mx_write_few_kernel(const MxMoveParams p)
   if (!u.there) return;
   const int lane = threadIdx.x & 31;
   const bool in_h = u.h < p.H;
-  const T* x = reinterpret_cast<const T*>(u.kind ? p.xv : p.xk) + blockIdx.y * p.st + (in_h ? u.h : 0) * p.sh +
-               (int64_t)u.q.row0 * p.sn + 4 * (lane % (D / 4));
-  const int64_t stream = ((int64_t)(p.first_step + blockIdx.y) * p.H + (in_h ? u.h : 0)) * p.L.pool_tiles;
+  const int h = in_h ? u.h : 0;
+  const int64_t xo = blockIdx.y * p.st + h * p.sh + (int64_t)u.q.row0 * p.sn + 4 * (lane % (D / 4));
+  const int64_t stream = ((int64_t)(p.first_step + blockIdx.y) * p.H + h) * p.L.pool_tiles;
   for (int quad = u.q.base >> 2; quad * 4 < u.q.ctx; ++quad) {
-    const int64_t pt = mx_pool_tile(p.L, blockIdx.z, quad >> 3, p.fault);
-    if (pt < 0) continue;
-    float v[4][4];
-    bool in[4];
+    MxRaw<T, 4, VEC> v[2][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int tok = quad * 4 + t;
-      in[t] = in_h && tok >= u.q.base && tok < u.q.ctx;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[t][j] = 0.f;
-      if (in[t]) load_channels<T, 4, VEC>(x + (int64_t)(tok - u.q.base) * p.sn, v[t]);
+      if (tok < u.q.base || tok >= u.q.ctx) continue;
+      v[0][t].load(reinterpret_cast<const T*>(p.xk) + xo + (int64_t)(tok - u.q.base) * p.sn);
+      v[1][t].load(reinterpret_cast<const T*>(p.xv) + xo + (int64_t)(tok - u.q.base) * p.sn);
     }
-    const Quad at((u.kind ? p.pv : p.pk) + (stream + pt) * MxTile<D, FMT>::kBytes, quad & 7, lane);
+    const int64_t pt = mx_pool_tile(p.L, blockIdx.z, quad >> 3, p.fault);
+    if (pt < 0) continue;
+    const Quad ak(p.pk + (stream + pt) * MxTile<D, FMT>::kBytes, quad & 7, lane);
+    const Quad av(p.pv + (stream + pt) * MxTile<D, FMT>::kBytes, quad & 7, lane);
     uint4 piece = {};
-    if (u.kind && in_h) piece = at.load_value();
+    if (in_h) piece = av.load_value();
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      uint32_t m = 0;
+      const int tok = quad * 4 + t;
+      if (tok < u.q.base || tok >= u.q.ctx) continue;
+      uint32_t m[2] = {v[0][t].peak(), v[1][t].peak()};
+      mx_peaks<T, 2, 1, 4>(m);
+      if (!in_h) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m = max(m, abs_bits(v[t][j]));
-#pragma unroll
-      for (int d = 1; d < 8; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-      if (!in[t]) continue;
-      float inv;
-      const uint32_t byte = mx_scale<FMT>(m, &inv);
-      const uint32_t code =
-          byte == kMxNan ? 0u : mx_codes4<FMT>(v[t][0] * inv, v[t][1] * inv, v[t][2] * inv, v[t][3] * inv);
-      if (u.kind) piece = Quad::with_token(piece, t, code);
-      else at.store_key(t, code);
-      if (at.l == 0) *at.scale(t) = (uint8_t)byte;
+      for (int kind = 0; kind < 2; ++kind) {
+        float inv;
+        const uint32_t byte = mx_scale<FMT>(m[kind], &inv);
+        const auto& w = v[kind][t];
+        const uint32_t code = byte == kMxNan ? 0u : mx_codes4<FMT>(w[0] * inv, w[1] * inv, w[2] * inv, w[3] * inv);
+        if (kind) piece = Quad::with_token(piece, t, code);
+        else ak.store_key(t, code);
+        if (ak.l == 0) *(kind ? av : ak).scale(t) = (uint8_t)byte;
+      }
     }
-    if (u.kind && in_h) at.store_value(piece);
+    if (in_h) av.store_value(piece);
   }
 }
 
@@ -579,33 +550,35 @@ __global__ void __launch_bounds__(256) mx_read_few_kernel(const MxMoveParams p) 
   const MxFew<D> u(p.L, p.H, p.fault);
   if (!u.there || u.h >= p.H) return;
   const int lane = threadIdx.x & 31;
-  T* x = reinterpret_cast<T*>(u.kind ? p.ov : p.ok) + blockIdx.y * p.st + u.h * p.sh + (int64_t)u.q.row0 * p.sn +
-         4 * (lane % (D / 4));
+  const int64_t xo = blockIdx.y * p.st + u.h * p.sh + (int64_t)u.q.row0 * p.sn + 4 * (lane % (D / 4));
   const int64_t stream = ((int64_t)(p.first_step + blockIdx.y) * p.H + u.h) * p.L.pool_tiles;
 #pragma unroll 2
   for (int quad = u.q.base >> 2; quad < (u.q.ctx + 3) >> 2; ++quad) {
     const int64_t pt = mx_pool_tile(p.L, blockIdx.z, quad >> 3, p.fault);
     if (pt < 0) continue;
-    const Quad at((u.kind ? p.pv : p.pk) + (stream + pt) * MxTile<D, FMT>::kBytes, quad & 7, lane);
-    const uint32_t sc = *reinterpret_cast<const uint32_t*>(at.scale(0));
-    uint4 piece = {};
-    if (u.kind) piece = at.load_value();
-    uint32_t w[4];
+    const Quad ak(p.pk + (stream + pt) * MxTile<D, FMT>::kBytes, quad & 7, lane);
+    const Quad av(p.pv + (stream + pt) * MxTile<D, FMT>::kBytes, quad & 7, lane);
+    const uint32_t sk = *reinterpret_cast<const uint32_t*>(ak.scale(0)), sv = *reinterpret_cast<const uint32_t*>(av.scale(0));
+    const uint4 piece = av.load_value();
+    uint32_t w[4] = {};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int tok = quad * 4 + t;
-      if (tok < u.q.base || tok >= u.q.ctx) continue;
-      w[t] = u.kind ? Quad::token(piece, t) : at.load_key(t);
+      if (tok >= u.q.base && tok < u.q.ctx) w[t] = ak.load_key(t);
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int tok = quad * 4 + t;
       if (tok < u.q.base || tok >= u.q.ctx) continue;
-      constexpr int kBits = FMT == LOOPVQ_MX_E4M3 ? 16 : 8;
-      const float2 a = mx_value2<FMT>(w[t] & ((1u << kBits) - 1)), b = mx_value2<FMT>(w[t] >> kBits);
-      const float s = mx_scale_value(sc >> (8 * t) & 255u);
-      const float v[4] = {a.x * s, a.y * s, b.x * s, b.y * s};
-      store_channels<T, 4, VEC>(x + (int64_t)(tok - u.q.base) * p.sn, v);
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {
+        constexpr int kBits = FMT == LOOPVQ_MX_E4M3 ? 16 : 8;
+        const uint32_t code = kind ? Quad::token(piece, t) : w[t];
+        const float2 a = mx_value2<FMT>(code & ((1u << kBits) - 1)), b = mx_value2<FMT>(code >> kBits);
+        const float s = mx_scale_value((kind ? sv : sk) >> (8 * t) & 255u);
+        const float v[4] = {a.x * s, a.y * s, b.x * s, b.y * s};
+        store_channels<T, 4, VEC>(reinterpret_cast<T*>(kind ? p.ov : p.ok) + xo + (int64_t)(tok - u.q.base) * p.sn, v);
+      }
     }
   }
 }
@@ -614,7 +587,7 @@ __global__ void __launch_bounds__(256) mx_read_few_kernel(const MxMoveParams p) 
 // memory, and only then writes them to their places: any order of indices is
 // safe, nothing is read after it was overwritten.
 constexpr int kMxKeepTiles = (kMxMaxTree + kMxTile - 2) / kMxTile + 1;   // that 64 tokens can touch
-constexpr int kMxKeepWarps = 4;
+constexpr int kMxKeepWarps = 2;
 
 struct MxKeepParams {
   MxLayout L;
@@ -628,10 +601,10 @@ struct MxKeepParams {
 template <int D, int FMT>
 __global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeepParams p) {
   using Quad = MxQuad<D, FMT>;
-  extern __shared__ __align__(16) uint32_t sm_all[];   // per warp: codes [room][32], scales [room][4] bytes
+  extern __shared__ __align__(16) uint32_t sm_all[];   // per warp: codes [room][K, V][32], scales [room][K, V][4] bytes
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t* code = sm_all + warp * p.room * 33;
-  uint8_t* scale = reinterpret_cast<uint8_t*>(code + p.room * 32);
+  uint32_t* code = sm_all + warp * p.room * 66;
+  uint8_t* scale = reinterpret_cast<uint8_t*>(code + p.room * 64);
   const MxFew<D> u(p.L, p.H, p.fault);
   if (!u.there) return;
   const int r = blockIdx.z, nk = __ldg(p.n_keep + r);
@@ -641,8 +614,7 @@ __global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeep
   }
   if (nk == 0) return;
   const bool in_h = u.h < p.H;
-  uint8_t* stream = (u.kind ? p.pv : p.pk) +
-                    ((int64_t)blockIdx.y * p.H + (in_h ? u.h : 0)) * p.L.pool_tiles * MxTile<D, FMT>::kBytes;
+  const int64_t stream = ((int64_t)blockIdx.y * p.H + (in_h ? u.h : 0)) * p.L.pool_tiles;
   const int t0 = u.q.base / kMxTile;
   int64_t tile_at[kMxKeepTiles];
 #pragma unroll
@@ -669,9 +641,14 @@ __global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeep
     const int f = __shfl_sync(0xffffffffu, i < 32 ? from[0] : from[1], i & 31);
     if (f < 0 || !in_h) continue;
     const int pos = u.q.base + f;
-    const Quad at(stream + tile_of(pos) * MxTile<D, FMT>::kBytes, (pos >> 2) & 7, lane);
-    code[i * 32 + lane] = u.kind ? Quad::token(at.load_value(), pos & 3) : at.load_key(pos & 3);
-    if (at.l == 0) scale[i * 4 + (lane >> 3)] = *at.scale(pos & 3);
+    const int64_t off = (stream + tile_of(pos)) * MxTile<D, FMT>::kBytes;
+    const Quad ak(p.pk + off, (pos >> 2) & 7, lane), av(p.pv + off, (pos >> 2) & 7, lane);
+    code[i * 64 + lane] = ak.load_key(pos & 3);
+    code[i * 64 + 32 + lane] = Quad::token(av.load_value(), pos & 3);
+    if (ak.l == 0) {
+      scale[i * 8 + (lane >> 3)] = *ak.scale(pos & 3);
+      scale[i * 8 + 4 + (lane >> 3)] = *av.scale(pos & 3);
+    }
   }
   const uint32_t moved[2] = {__ballot_sync(0xffffffffu, from[0] >= 0), __ballot_sync(0xffffffffu, from[1] >= 0)};
   __syncwarp();
@@ -679,28 +656,30 @@ __global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeep
   for (int quad = u.q.base >> 2; quad * 4 < u.q.base + nk; ++quad) {
     const int64_t pt = tile_of(quad * 4);
     if (pt < 0) continue;
-    const Quad at(stream + pt * MxTile<D, FMT>::kBytes, quad & 7, lane);
-    uint4 piece = {};
-    if (u.kind) piece = at.load_value();
+    const int64_t off = (stream + pt) * MxTile<D, FMT>::kBytes;
+    const Quad ak(p.pk + off, quad & 7, lane), av(p.pv + off, quad & 7, lane);
+    uint4 piece = av.load_value();
     bool any = false;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int i = quad * 4 + t - u.q.base;
       if (i < 0 || i >= nk || !(moved[i >> 5] >> (i & 31) & 1)) continue;
       any = true;
-      const uint32_t w = code[i * 32 + lane];
-      if (u.kind) piece = Quad::with_token(piece, t, w);
-      else at.store_key(t, w);
-      if (at.l == 0) *at.scale(t) = scale[i * 4 + (lane >> 3)];
+      ak.store_key(t, code[i * 64 + lane]);
+      piece = Quad::with_token(piece, t, code[i * 64 + 32 + lane]);
+      if (ak.l == 0) {
+        *ak.scale(t) = scale[i * 8 + (lane >> 3)];
+        *av.scale(t) = scale[i * 8 + 4 + (lane >> 3)];
+      }
     }
-    if (u.kind && any) at.store_value(piece);
+    if (any) av.store_value(piece);
   }
 }
 
-// Blocks of `warps` warps over the heads of K and V.
+// Blocks of `warps` warps over the heads.
 unsigned few_blocks(const loopvq_mx_desc* d, int warps) {
   const int heads = 128 / d->head_dim, groups = (d->n_heads_kv + heads - 1) / heads;
-  return (unsigned)((2 * groups + warps - 1) / warps);
+  return (unsigned)((groups + warps - 1) / warps);
 }
 
 loopvq_status move_setup(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout, int32_t first_step,
@@ -871,7 +850,7 @@ extern "C" loopvq_status loopvq_mx_keep(const loopvq_mx_desc* desc, const loopvq
   p.fault = fault_bits;
   const dim3 grid(few_blocks(desc, kMxKeepWarps), desc->n_loop, p.L.batch);
   p.room = max_keep < layout->max_new ? max_keep : layout->max_new;
-  const size_t smem = (size_t)kMxKeepWarps * p.room * 33 * sizeof(uint32_t);   // at most 33,792 bytes
+  const size_t smem = (size_t)kMxKeepWarps * p.room * 66 * sizeof(uint32_t);   // at most 33,792 bytes
   auto kfn = desc->head_dim == 128
                  ? (desc->format == LOOPVQ_MX_E4M3 ? mx_keep_kernel<128, LOOPVQ_MX_E4M3> : mx_keep_kernel<128, LOOPVQ_MX_E2M1>)
                  : (desc->format == LOOPVQ_MX_E4M3 ? mx_keep_kernel<64, LOOPVQ_MX_E4M3> : mx_keep_kernel<64, LOOPVQ_MX_E2M1>);
