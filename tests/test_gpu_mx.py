@@ -292,6 +292,104 @@ def test_attention_many_rows(types, n, Hq):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("kind", ["tree", "chain", "cap_bias"])
+def test_attention_on_the_tensor_cores(fmt, D, kind):
+    """More rows than the warps' kernel takes: whole and partial chunks, requests
+    with few rows or none beside them, contexts of the new tokens alone, tile
+    borders, units that spread over several blocks."""
+    new = [64, 0, 33, 1, 50, 64]
+    s = Setup([64, 10, 33 + 31, 200, 3000, 97], new, D=D, fmt=fmt, H=2, Hq=8, seed=D + len(kind), page=96)
+    K, V = _filled(s)
+    q = _queries(s, "bf16")
+    masks = None if kind == "chain" else [_tree(s.rng, n) for n in new]
+    cap, slopes = 0.0, None
+    if kind == "cap_bias":
+        cap, slopes = 8.0, torch.tensor([2.0 ** -(i + 1) for i in range(8)], device="cuda")
+    o, l = _run(s, q, masks, cap=cap, slopes=slopes)
+    _check(s, q, K, V, masks, o, l, cap=cap, slopes=slopes)
+    again = _run(s, q, masks, cap=cap, slopes=slopes)
+    assert np.array_equal(o, again[0]) and np.array_equal(l, again[1]) and s.faults() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_tensor_core_rows_see_only_their_own(fmt):
+    """NaN and infinite siblings, 0xFF bytes behind the contexts, rows that see
+    nothing, a page outside the pool; then scores that rise by more than the
+    slack from tile to tile, so that the sums are rescaled."""
+    n, G = 60, 3
+    s = Setup([200 + n, n + 5], [n, n], D=64, fmt=fmt, H=1, Hq=G, seed=30, page=32)
+    K = [_values(s.rng, (1, c, 1, 64), "k") for c in s.ctx]
+    V = [_values(s.rng, (1, c, 1, 64), "v") for c in s.ctx]
+    K[0][0, 200 + 7, 0, 5] = np.nan
+    V[0][0, 200 + 9, 0, 40] = np.inf
+    V[1][0, 2, 0, 3] = np.nan            # in a prefix: every row sees it
+    s.write_all(K, V)
+    back = [[O.mx_values(*O.mx_quantise(x[0], fmt), fmt) for x in X] for X in (K, V)]
+    masks = [_tree(s.rng, n) for _ in s.ctx]
+    masks[0][11] = 0
+    masks[0][13] |= 1 << 7
+    masks[0][14] |= 1 << 9
+    q = _queries(s, "bf16")
+    o, l = _run(s, q, masks)
+    _check(s, q, *back, masks, o, l)
+    assert np.isnan(o[14]).any() and np.isfinite(o[0]).all() and np.isnan(o[n:, :, :32]).all()
+    hole = s.table[0, 2]
+    s.table[0, 2] = -1
+    lay = s.layout(s.ctx, s.off)
+    o, l = _run(s, q, masks, lay=lay)
+    s.table[0, 2] = hole
+    assert s.faults() == L.LOOPVQ_FAULT_POOL_RANGE
+    written = [np.ones(c, dtype=bool) for c in s.ctx]
+    written[0][64:96] = False
+    _check(s, q, *back, masks, o, l, written=written)
+    s.fault.zero_()
+    o, l = _run(s, q, masks, lay=s.layout([260, 10 ** 6], s.off, max_ctx_len=260))
+    assert s.faults() == L.LOOPVQ_FAULT_CTX_RANGE and (o[n:] == 7).all()
+    # rising and falling scores
+    s = Setup([1500], [n], D=64, fmt="e4m3", H=1, Hq=G, seed=31)
+    K = [np.zeros((1, 1500, 1, 64), dtype=np.float32)]
+    K[0][0, :, 0, 0] = np.concatenate([np.linspace(-300, 300, 1000), np.linspace(300, -300, 500)])
+    V = [_values(s.rng, (1, 1500, 1, 64), "v") * np.exp2(s.rng.integers(-20, 20, (1, 1500, 1, 1)))]
+    s.write_all(K, V)
+    back = [[O.mx_values(*O.mx_quantise(x[0], "e4m3"), "e4m3") for x in X] for X in (K, V)]
+    q = np.zeros((n, G, 64), dtype=np.float32)
+    q[:, :, 0] = torch.from_numpy(s.rng.uniform(-1, 1, (n, G)).astype(np.float32)).to(torch.bfloat16).float().numpy()
+    o, l = _run(s, q, None, scale=1.0)
+    _check(s, q, *back, None, o, l, scale=1.0)
+
+
+def test_tensor_core_blocks_far_apart():
+    """Blocks of one token 2^30 apart: on the tensor cores the small one is rounded
+    to 2^-24 of the token's largest scale, 2^-25 of 2^E at most, and 2^E is at most
+    twice the token's largest value over the top of the format."""
+    n, G = 64, 2
+    s = Setup([300], [n], D=128, fmt="e4m3", H=1, Hq=G, seed=32)
+    K = [_values(s.rng, (1, 300, 1, 128), "k")]
+    V = [_values(s.rng, (1, 300, 1, 128), "v")]
+    V[0][..., 32:64] *= 2.0 ** -30
+    V[0][..., 64:96] *= 2.0 ** -12
+    s.write_all(K, V)
+    k, v = (O.mx_values(*O.mx_quantise(x[0][0], "e4m3"), "e4m3") for x in (K, V))
+    q = _queries(s, "bf16")
+    o, l = _run(s, q, None)
+    big = np.abs(v[:, 0]).max(-1)
+    sees = np.tril(np.ones((n, 300), dtype=bool), 300 - n)
+    for hq in range(G):
+        qq = q[:, hq].astype(np.float64)
+        ref, _, a, top = O.mx_attention(qq, k[:, 0], v[:, 0], sees, None, None, 128 ** -0.5)
+        x = np.where(sees, 128 ** -0.5 * (qq @ k[:, 0].T), -np.inf)
+        p = np.exp(x - x.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        B = 128 ** -0.5 * (np.abs(qq) @ np.abs(k[:, 0]).T).max(-1, keepdims=True)
+        w = 2 * (32 * 2.0 ** -24 + 2.0 ** -22) * B + 2.0 ** -22 + 2.0 ** -11 + 2.0 ** -17
+        # a weight holds the token's factor here: its end is 2^-33 of the largest weight of the row, times codes up to the top
+        floor = 300 * 2.0 ** -32 * (p * big).max(-1, keepdims=True) + 2.0 ** -25 * 2 / 448 * (p @ big)[:, None]
+        assert (np.abs(o[:, hq] - ref) <= a * w + floor + 2.0 ** -8 * np.abs(ref)).all()
+        assert (np.abs(o[:, hq, 64:96] - ref[:, 64:96]) <= (a * w + floor + 2.0 ** -8 * np.abs(ref))[:, 64:96]).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_masks_of_every_kind(fmt):
     """Rows that see nothing, bits beyond the new tokens, a row that does not see
     itself, one that sees a later token."""
@@ -388,9 +486,9 @@ def test_queries_of_any_size_and_order():
     assert np.array_equal(o[keep], o2[keep])
 
 
-@pytest.mark.parametrize("ctx", [20000, 40001])
-def test_attention_long(ctx):
-    s = Setup([ctx, 77], [1, 1], fmt="e2m1", H=1, Hq=2, seed=8, page=256)
+@pytest.mark.parametrize("ctx,new", [(20000, 1), (40001, 1), (20000, 6), (20011, 64)])
+def test_attention_long(ctx, new):
+    s = Setup([ctx, 77], [new, 1], fmt="e2m1", H=1, Hq=2, seed=8, page=256)
     K, V = _filled(s)
     q = _queries(s, "bf16")
     o, l = _run(s, q, None)
