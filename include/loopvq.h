@@ -601,6 +601,8 @@ typedef struct {
  * new_off[r+1]-1 of every packed argument (x, q, out, tree_mask) are theirs,
  * in order.  A decode step has n_r = 1, a prompt its whole length, a tree of
  * drafted tokens its nodes, an idle request 0.
+ * The arrays are read on the device when the kernels run and must not change
+ * before they end.
  * Faults (LOOPVQ_FAULT_* bits ORed into fault_bits, a device uint32 that the
  * caller zeroes, or NULL): a ctx_len or new_off out of its bounds
  * (CTX_RANGE) leaves that request out, its rows and tokens as they were; a
@@ -677,9 +679,14 @@ LOOPVQ_API size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, con
  * A token that sees nothing gets a zero output and lse -inf.  What a token
  * does not see never reaches its output, whatever the pool holds there.
  * Scores are fp32 sums of exact products of codes and q (q in fp32: to 22
- * bits); softmax statistics are fp32; the weights meet the values in fp16
- * (11 bits) for a bf16 output and as two fp16 terms (22 bits) for fp32.
- * Launches one kernel, or two when long contexts are split.
+ * bits; elements below 2^-28 of their row's largest to 2^-38 of it); softmax
+ * statistics are fp32; the weights meet the values in fp16 (11 bits) for bf16
+ * q and out, and as two fp16 terms (22 bits) else.  With bf16 q and out and
+ * many rows (tokens x query heads of a KV head: more than 40 for D = 128, 64
+ * for D = 64) the tensor cores take keys and values to 2^-24 of 2^E, E the
+ * token's largest scale exponent: exact unless its blocks are 2^15 apart.
+ * Results do not depend on what else runs; the same call gives the same bits.
+ * Launches two kernels, of which the second adds up split contexts.
  */
 LOOPVQ_API loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
                                         const void* poolK, const void* poolV, const void* q, loopvq_dtype q_dtype,
