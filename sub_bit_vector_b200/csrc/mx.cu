@@ -33,13 +33,14 @@ struct MxMoveParams {
 // Scale byte of a block with largest magnitude bits m, and 2^-e.
 template <int FMT>
 __device__ __forceinline__ uint32_t mx_scale(uint32_t m, float* inv) {
-  // top = 1.75 * 2^8 or 1.5 * 2^2: e = exponent - 8 (2), one more above top's fraction
-  constexpr int kTopExp = FMT == LOOPVQ_MX_E4M3 ? 8 : 2;
+  // top = 1.75 * 2^8 or 1.5 * 2^2: e + 127 = exponent field - 8 (2), one more
+  // above top's fraction, which the addition carries
+  constexpr uint32_t kTopExp = FMT == LOOPVQ_MX_E4M3 ? 8 : 2;
   constexpr uint32_t kTopFrac = FMT == LOOPVQ_MX_E4M3 ? 0x600000u : 0x400000u;
-  int e = (int)(m >> 23) - 127 - kTopExp + ((m & 0x7fffffu) > kTopFrac ? 1 : 0);
-  e = max(kMxExpMin, min(kMxExpMax, e));
-  *inv = __uint_as_float((uint32_t)(127 - e) << 23);
-  return m >= 0x7f800000u ? kMxNan : (uint32_t)(e + 127);
+  const int f = (int)((m + (0x7fffffu - kTopFrac)) >> 23) - (int)kTopExp;
+  const uint32_t byte = (uint32_t)max(kMxExpMin + 127, min(kMxExpMax + 127, f));
+  *inv = __uint_as_float((254u - byte) << 23);
+  return m >= 0x7f800000u ? kMxNan : byte;
 }
 // Four scaled values to codes: e4m3 in the 4 bytes, e2m1 in the low 4 nibbles.
 template <int FMT>

@@ -14,8 +14,8 @@
 // an element is rounded to 2^-24 of 2^E, which is less than 2^-26 of its token's
 // largest element.  A block of NaN counts as 0 in V' and is put into the outputs
 // of the rows that see it at the end.
-// Four warps convert codes, and two of them issue the products; four compute the softmax (and one
-// thread of them issues the copies); operands, scores and weights are double-buffered, so that tile i's
+// Four warps convert codes, one of which issues the scores' product; four
+// compute the softmax, one of which issues P V and another the copies; operands, scores and weights are double-buffered, so that tile i's
 // softmax, tile i + 1's scores and the product P V of tile i - 1 run together.
 //
 // Operands in shared memory are K-major without swizzle: core matrices of 8
@@ -56,7 +56,7 @@ struct RowsInfo {
     uint32_t hidden;       // the page is not in the pool
   } t[2];
   uint64_t full[4], freed[4];                     // raw tiles: arrived, read
-  uint64_t told[2], scores[2], weights[2], sums[2];   // info written; S, P, O += P V done
+  uint64_t told[2], ready[2], scores[2], weights[2], sums[2];   // info, V' written; S, P, O += P V done
   uint64_t query;                                 // Q written
   uint32_t tmem, bad;
 };
@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&I.told[i]), 4);
+      mbar_init(smem_u32(&I.ready[i]), 4);
       mbar_init(smem_u32(&I.scores[i]), 1);
       mbar_init(smem_u32(&I.weights[i]), 128);
       mbar_init(smem_u32(&I.sums[i]), 1);
@@ -201,10 +202,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
   if (warp >= 4) {
     // ======================== conversion, copies, products
     const int w4 = __shfl_sync(0xffffffffu, warp - 4, 0);
-    const bool leader = w4 == 0, adder = w4 == 2;   // these warps issue S and P V
+    const bool leader = w4 == 0;   // issues S
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t desc_k = smem_desc(smem_u32(sm + R::kK), R::kKLbo, R::kKSbo);
-    const uint64_t desc_v = smem_desc(smem_u32(sm + R::kV), R::kVLbo, R::kVSbo);
     const int sub = w4 >> 1;
     constexpr int UB = NB / 2;   // blocks of a warp, of one half of the tile
     const int b0 = (w4 & 1) * UB;
@@ -222,20 +222,6 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
     };
     bool go = true;
     int units = 0;
-    // O += P V of tile i, once its weights are there
-    auto product = [&](int i, bool fresh) {
-      ok &= wait2(I.weights, i);
-      if (adder) {
-        __syncwarp();
-        tmem_after();
-        const uint32_t el = elect();
-        const uint64_t dv = desc_v + (uint64_t)(i & 1) * (R::kVBuf >> 4);
-        const uint32_t pa = tm + R::kS + kMxTile * (i & 1);
-        umma_ts(tm + R::kO, pa, dv, idesc(D), !fresh, el);
-        umma_ts(tm + R::kO, pa + 8, dv + (2 * R::kVLbo >> 4), idesc(D), 1, el);
-        umma_commit(smem_u32(&I.sums[i & 1]), el);
-      }
-    };
     while (done < count && go) {
       MxReq rq = {};
       mx_request(p.L, cc.r, &rq, nullptr);
@@ -248,7 +234,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         const bool edge = tok0 + kMxTile > rq.base;
         ok &= mbar_wait_bounded(smem_u32(&I.full[slot]), phase);
         const bool bad = *reinterpret_cast<volatile uint32_t*>(&I.bad) >> slot & 1;
-        // (K' of tile i - 2 has been read: its weights were waited for)
+        if (i >= 2) ok &= wait2(I.sums, i - 2);   // so nothing of tile i - 2 is needed any more
         const uint8_t* const sk = sm + R::kRing + slot * R::kSlot;
         const uint8_t* const sv = sk + Tile::kBytes;
         uint32_t w[UB][4], wv[UB][4];   // e4m3: 4 words of a block; e2m1: 2
@@ -334,7 +320,6 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         if (!(go = sync4())) break;
         if (leader) {
           if (it == 0) ok &= mbar_wait_bounded(smem_u32(&I.query), (uint32_t)units & 1);
-          if (i >= 2) ok &= wait2(I.sums, i - 2);   // P of tile i - 2, where S goes, has been read
           __syncwarp();
           tmem_after();
           const uint32_t el = elect();
@@ -346,7 +331,6 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         }
         // ---- V'
         const float4 ve = *reinterpret_cast<const float4*>(T.vfac + sub * 16 + 4 * c);   // of this lane's tokens
-        if (i >= 2) ok &= wait2(I.sums, i - 2);   // V' of tile i - 2 has been read
         uint8_t* const dv = sm + R::kV + (i & 1) * R::kVBuf;
 #pragma unroll
         for (int k = 0; k < UB; ++k) {
@@ -371,14 +355,15 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
           }
         }
         fence_proxy_async();
-        if (!(go = sync4())) break;   // the raw tile has been read, V' is written
-        if (lane == 0) mbar_arrive(smem_u32(&I.freed[slot]));
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&I.ready[i & 1]));
+          mbar_arrive(smem_u32(&I.freed[slot]));
+        }
         if (++slot == S) {
           slot = 0;
           phase ^= 1;
         }
-        if (it > 0) product(i - 1, it == 1);
-        if (it == n_tiles - 1) product(i, it == 0);
         ++done;
       }
       ++units;
@@ -389,6 +374,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
     // ======================== softmax: a thread has a row
     const int tid = threadIdx.x;
     const uint32_t mine = tmem + ((uint32_t)(warp * 32) << 16);   // this warp's lanes
+    const bool adder = __shfl_sync(0xffffffffu, warp, 0) == 0;    // issues P V
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t desc_v = smem_desc(smem_u32(sm + R::kV), R::kVLbo, R::kVSbo);
     MxCursor pc = cc;            // the copier's: the next tile
     const int per = p.L.page_tokens / kMxTile;
     int page = pc.t / per, in_page = pc.t % per, issued = 0;
@@ -592,6 +580,17 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         tmem_wait_st();
         tmem_before();
         mbar_arrive(smem_u32(&I.weights[i & 1]));
+        if (adder) {   // O += P V'
+          ok &= wait2(I.ready, i);
+          ok &= wait2(I.weights, i);
+          __syncwarp();
+          tmem_after();
+          const uint32_t el = elect(), pa = tm + R::kS + kMxTile * (i & 1);
+          const uint64_t dv = desc_v + (uint64_t)(i & 1) * (R::kVBuf >> 4);
+          umma_ts(tm + R::kO, pa, dv, idesc(D), it > 0, el);
+          umma_ts(tm + R::kO, pa + 8, dv + (2 * R::kVLbo >> 4), idesc(D), 1, el);
+          umma_commit(smem_u32(&I.sums[i & 1]), el);
+        }
         if (copier) {   // refill the ring where the conversion has read it
           ok &= mbar_wait_bounded(smem_u32(&I.freed[slot]), phase);
           if (*reinterpret_cast<volatile uint32_t*>(&I.bad) >> slot & 1) atomicAnd(&I.bad, ~(1u << slot));
