@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         const bool edge = tok0 + kMxTile > rq.base;
         ok &= mbar_wait_bounded(smem_u32(&I.full[slot]), phase);
         const bool bad = *reinterpret_cast<volatile uint32_t*>(&I.bad) >> slot & 1;
-        if (i >= 2) ok &= wait2(I.sums, i - 2);   // so nothing of tile i - 2 is needed any more
+        if (i >= 2) ok &= wait2(I.weights, i - 2);   // K' and the info of tile i - 2 have been read
         const uint8_t* const sk = sm + R::kRing + slot * R::kSlot;
         const uint8_t* const sv = sk + Tile::kBytes;
         uint32_t w[UB][4], wv[UB][4];   // e4m3: 4 words of a block; e2m1: 2
@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         if (!(go = sync4())) break;
         if (leader) {
           if (it == 0) ok &= mbar_wait_bounded(smem_u32(&I.query), (uint32_t)units & 1);
+          if (i >= 2) ok &= wait2(I.sums, i - 2);   // P of tile i - 2, where S goes, has been read
           __syncwarp();
           tmem_after();
           const uint32_t el = elect();
@@ -331,6 +332,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         }
         // ---- V'
         const float4 ve = *reinterpret_cast<const float4*>(T.vfac + sub * 16 + 4 * c);   // of this lane's tokens
+        if (i >= 2) ok &= wait2(I.sums, i - 2);   // V' of tile i - 2 has been read
         uint8_t* const dv = sm + R::kV + (i & 1) * R::kVBuf;
 #pragma unroll
         for (int k = 0; k < UB; ++k) {
@@ -524,9 +526,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
           const uint2 z = *reinterpret_cast<const uint2*>(T.nan);
           poison |= (z.x & vis ? 1u : 0u) | (z.y & vis ? 2u : 0u);
         }
-        float top = -INFINITY;
+        float tops[4] = {x[0], x[1], x[2], x[3]};   // four chains
 #pragma unroll
-        for (int t = 0; t < 32; ++t) top = fmaxf(top, x[t]);
+        for (int t = 4; t < 32; ++t) tops[t & 3] = fmaxf(tops[t & 3], x[t]);
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
         // ---- raise the references if a score or a weight could leave its range
         const bool over = top > m + kScoreSlack || ex2(top - (m == -INFINITY ? 0.f : m)) * fmaxf(fmaxf(T.vmax[0], T.vmax[1]), fmaxf(T.vmax[2], T.vmax[3])) * rs > kWeightMax;
         if (__any_sync(0xffffffffu, over)) {   // (all lanes: the TMEM accesses are the warp's)
@@ -561,20 +564,21 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         // ---- weights
         const float mi = m == -INFINITY ? 0.f : m;
         const float2 r2 = make_float2(rs, rs), n2 = make_float2(-mi, -mi);
-        float2 sum = make_float2(0.f, 0.f);
+        float2 sum = make_float2(0.f, 0.f), sum2 = sum;
         uint32_t pw[16];
 #pragma unroll
         for (int t = 0; t < 32; t += 4) {
           float2 y = add2(make_float2(x[t], x[t + 1]), n2), z = add2(make_float2(x[t + 2], x[t + 3]), n2);
           y = make_float2(ex2(y.x), ex2(y.y));
           z = make_float2(ex2(z.x), ex2(z.y));
-          sum = add2(sum, add2(y, z));
+          sum = add2(sum, y);
+          sum2 = add2(sum2, z);
           const float4 sc = *reinterpret_cast<const float4*>(T.vfac + t);
           const float2 wy = mul2(mul2(y, make_float2(sc.x, sc.y)), r2), wz = mul2(mul2(z, make_float2(sc.z, sc.w)), r2);
           pw[t / 2] = pack_f16(wy.x, wy.y);
           pw[t / 2 + 1] = pack_f16(wz.x, wz.y);
         }
-        l += sum.x + sum.y;
+        l += (sum.x + sum.y) + (sum2.x + sum2.y);
         __syncwarp();
         tmem_st16(mine + R::kS + kMxTile * (i & 1), pw);   // S has been read; P of tile i - 2 was, before S was written
         tmem_wait_st();
