@@ -606,7 +606,8 @@ typedef struct {
  * Faults (LOOPVQ_FAULT_* bits ORed into fault_bits, a device uint32 that the
  * caller zeroes, or NULL): a ctx_len or new_off out of its bounds
  * (CTX_RANGE) leaves that request out, its rows and tokens as they were; a
- * page id outside the pool (POOL_RANGE) leaves out that page's tokens.
+ * page id outside the pool (POOL_RANGE) leaves out that page's tokens; a
+ * bounded wait that gave up sets TIMEOUT, and the call's output is undefined.
  * Pages written in one call must not be shared between its requests.
  */
 typedef struct {
@@ -659,7 +660,8 @@ LOOPVQ_API size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, con
  * Attention of each request's new tokens (at most 64: one token, or a tree or
  * chain of drafted ones, whose keys and values are in the cache already) over
  * its context at one loop step.  With P = ctx_len - n_r, new token i sees the
- * prefix p < P and the new tokens j with bit j of its mask set:
+ * prefix p < P and the new tokens j with bit j of its mask set (the scores
+ * have to be finite in fp32):
  *   s = softmax_scale * q . k;  s = softcap * tanh(s / softcap) if softcap > 0;
  *   s = s - slopes[hq] * (pos_i - pos_n) if slopes is given;
  *   o = sum_n softmax(s)_n v_n

@@ -408,10 +408,13 @@ def _prepared(name, args, keep, stream):
     plain = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t)
     args = tuple(t(a) if t in plain else a for t, a in zip(fn.argtypes, args))     # converted once
     # the current stream of the buffers' device: a tenth of the cost of torch.cuda.current_stream()
-    current, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device()
+    current, here = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    device = here()
     at = None if stream is None else _stream(stream)
 
     def call():
+        if here() != device:
+            raise ValueError(f"{name} was prepared on cuda:{device}, which is not the current device")
         st = fn(*args, current(device) if at is None else at)
         if st != LOOPVQ_OK:
             raise LoopVQError(name, st)
@@ -426,8 +429,9 @@ def loopvq_mx_pool_bytes(desc, pool_tokens: int) -> int:
 def prepare_mx_write(desc, layout, first_step, n_steps, k, v, stride_t, stride_n, stride_h, poolK, poolV,
                      fault_bits=None, stream=None):
     """loopvq_mx_write with every argument checked and marshalled once:
-    returns a zero-argument callable that issues the call.  The tensors must
-    stay in place; their contents may change between calls."""
+    returns a zero-argument callable that issues the call, without a stream on
+    the one that is current then.  The tensors must stay in place; their
+    contents may change between calls."""
     _here(k, v, poolK, poolV, *layout._keep)
     _mx_pools(desc, layout, poolK, poolV)
     _mx_rows(desc, layout, first_step, n_steps, k, v, stride_t, stride_n, stride_h)
