@@ -194,6 +194,7 @@ template <int D, int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) mx_write_kernel(const MxMoveParams p) {
   using Tile = MxTile<D, FMT>;
   constexpr int NB = Tile::kBlocks;
+  mx_begin();
   MxUnit u;
   if (!mx_unit<D, FMT>(p, &u)) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -343,6 +344,7 @@ template <int D, int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_read_kernel(const MxMoveParams p) {
   using Tile = MxTile<D, FMT>;
   constexpr int NB = Tile::kBlocks;
+  mx_begin();
   MxUnit u;
   if (!mx_unit<D, FMT>(p, &u)) return;
   const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -501,6 +503,7 @@ struct MxFew {
 template <int D, int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_write_few_kernel(const MxMoveParams p) {
   using Quad = MxQuad<D, FMT>;
+  mx_begin();
   const MxFew<D> u(p.L, p.H, p.fault);
   if (!u.there) return;
   const int lane = threadIdx.x & 31;
@@ -548,6 +551,7 @@ __global__ void __launch_bounds__(256) mx_write_few_kernel(const MxMoveParams p)
 template <int D, int FMT, typename T, bool VEC>
 __global__ void __launch_bounds__(256) mx_read_few_kernel(const MxMoveParams p) {
   using Quad = MxQuad<D, FMT>;
+  mx_begin();
   const MxFew<D> u(p.L, p.H, p.fault);
   if (!u.there || u.h >= p.H) return;
   const int lane = threadIdx.x & 31;
@@ -606,6 +610,7 @@ __global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeep
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* code = sm_all + warp * p.room * 66;
   uint8_t* scale = reinterpret_cast<uint8_t*>(code + p.room * 64);
+  mx_begin();
   const MxFew<D> u(p.L, p.H, p.fault);
   if (!u.there) return;
   const int r = blockIdx.z, nk = __ldg(p.n_keep + r);
@@ -761,11 +766,11 @@ using namespace loopvq;
 #define MX_BY_TYPE(KERNEL, GRID, STREAM, P, T, V)                                                     \
   do {                                                                                                \
     if (desc->head_dim == 128) {                                                                      \
-      if (desc->format == LOOPVQ_MX_E4M3) KERNEL<128, LOOPVQ_MX_E4M3, T, V><<<GRID, 256, 0, STREAM>>>(P); \
-      else KERNEL<128, LOOPVQ_MX_E2M1, T, V><<<GRID, 256, 0, STREAM>>>(P);                             \
+      if (desc->format == LOOPVQ_MX_E4M3) st = mx_launch(KERNEL<128, LOOPVQ_MX_E4M3, T, V>, GRID, 256, 0, STREAM, P); \
+      else st = mx_launch(KERNEL<128, LOOPVQ_MX_E2M1, T, V>, GRID, 256, 0, STREAM, P);                             \
     } else {                                                                                          \
-      if (desc->format == LOOPVQ_MX_E4M3) KERNEL<64, LOOPVQ_MX_E4M3, T, V><<<GRID, 256, 0, STREAM>>>(P);  \
-      else KERNEL<64, LOOPVQ_MX_E2M1, T, V><<<GRID, 256, 0, STREAM>>>(P);                              \
+      if (desc->format == LOOPVQ_MX_E4M3) st = mx_launch(KERNEL<64, LOOPVQ_MX_E4M3, T, V>, GRID, 256, 0, STREAM, P);  \
+      else st = mx_launch(KERNEL<64, LOOPVQ_MX_E2M1, T, V>, GRID, 256, 0, STREAM, P);                              \
     }                                                                                                 \
   } while (0)
 #define MX_MOVE(KERNEL, DTYPE, A, B)                                                   \
@@ -792,9 +797,10 @@ extern "C" loopvq_status loopvq_mx_write(const loopvq_mx_desc* desc, const loopv
                                          loopvq_stream_t stream) {
   MxMoveParams p = {};
   dim3 grid;
-  const loopvq_status st = move_setup(desc, layout, first_step, n_steps, x_dtype, stride_t, stride_n, stride_h,
+  const loopvq_status bad = move_setup(desc, layout, first_step, n_steps, x_dtype, stride_t, stride_n, stride_h,
                                       poolK, poolV, fault_bits, &p, &grid);
-  if (st != LOOPVQ_OK) return st;
+  if (bad != LOOPVQ_OK) return bad;
+  cudaError_t st = cudaSuccess;
   if (layout->total_new == 0 || layout->max_new == 0 || layout->max_ctx_len == 0) return LOOPVQ_OK;
   const uintptr_t es = x_dtype == LOOPVQ_BF16 ? 2 : 4;
   if (!k || !v || (uintptr_t)k % es || (uintptr_t)v % es) return LOOPVQ_ERR_INVALID_ARG;
@@ -802,7 +808,7 @@ extern "C" loopvq_status loopvq_mx_write(const loopvq_mx_desc* desc, const loopv
   p.xv = v;
   if (p.few) MX_MOVE(mx_write_few_kernel, x_dtype, k, v);
   else MX_MOVE(mx_write_kernel, x_dtype, k, v);
-  return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+  return st == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }
 
 extern "C" loopvq_status loopvq_mx_read(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
@@ -812,9 +818,10 @@ extern "C" loopvq_status loopvq_mx_read(const loopvq_mx_desc* desc, const loopvq
                                         loopvq_stream_t stream) {
   MxMoveParams p = {};
   dim3 grid;
-  const loopvq_status st = move_setup(desc, layout, first_step, n_steps, out_dtype, stride_t, stride_n, stride_h,
+  const loopvq_status bad = move_setup(desc, layout, first_step, n_steps, out_dtype, stride_t, stride_n, stride_h,
                                       poolK, poolV, fault_bits, &p, &grid);
-  if (st != LOOPVQ_OK) return st;
+  if (bad != LOOPVQ_OK) return bad;
+  cudaError_t st = cudaSuccess;
   if (layout->total_new == 0 || layout->max_new == 0 || layout->max_ctx_len == 0) return LOOPVQ_OK;
   const uintptr_t es = out_dtype == LOOPVQ_BF16 ? 2 : 4;
   if (!k_out || !v_out || (uintptr_t)k_out % es || (uintptr_t)v_out % es) return LOOPVQ_ERR_INVALID_ARG;
@@ -826,7 +833,7 @@ extern "C" loopvq_status loopvq_mx_read(const loopvq_mx_desc* desc, const loopvq
   p.ov = v_out;
   if (p.few) MX_MOVE(mx_read_few_kernel, out_dtype, k_out, v_out);
   else MX_MOVE(mx_read_kernel, out_dtype, k_out, v_out);
-  return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+  return st == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }
 
 extern "C" loopvq_status loopvq_mx_keep(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
@@ -855,6 +862,5 @@ extern "C" loopvq_status loopvq_mx_keep(const loopvq_mx_desc* desc, const loopvq
   auto kfn = desc->head_dim == 128
                  ? (desc->format == LOOPVQ_MX_E4M3 ? mx_keep_kernel<128, LOOPVQ_MX_E4M3> : mx_keep_kernel<128, LOOPVQ_MX_E2M1>)
                  : (desc->format == LOOPVQ_MX_E4M3 ? mx_keep_kernel<64, LOOPVQ_MX_E4M3> : mx_keep_kernel<64, LOOPVQ_MX_E2M1>);
-  kfn<<<grid, kMxKeepWarps * 32, smem, (cudaStream_t)stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
+  return mx_launch(kfn, grid, kMxKeepWarps * 32, smem, (cudaStream_t)stream, p) == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }

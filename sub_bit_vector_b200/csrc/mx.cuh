@@ -75,6 +75,28 @@ __device__ __forceinline__ int64_t mx_pool_tile(const MxLayout& L, int r, int t,
   return (int64_t)id * per + t % per;
 }
 
+// The kernels of a step follow one another closely: each may be launched while
+// the one before it ends.  Nothing is read or written, and no kernel after this
+// one is let in, before that one has ended.
+__device__ __forceinline__ void mx_begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename K, typename P>
+cudaError_t mx_launch(K kernel, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // Host checks shared by the entry points.
 loopvq_status mx_check_desc(const loopvq_mx_desc* d);
 loopvq_status mx_check_layout(const loopvq_mx_layout* l, MxLayout* out);

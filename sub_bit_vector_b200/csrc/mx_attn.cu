@@ -90,7 +90,7 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
   const int gb = NARROW ? g % NB : 0;                  // this lane's block,
   const int gr = NARROW ? g / NB % RPG : g;            // row in a group,
   const int half = NARROW == 2 ? g >> 2 : 0;           // half of the tile (NARROW 2)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  mx_begin();
   const int n_warps = p.n_workers, wid = blockIdx.x * W + warp;
 
   // each warp's share of the list: `extra` warps take one tile more than the others
@@ -657,7 +657,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttn
   constexpr int kCh = D / 32;   // channels of a lane
   __shared__ float sm_o[kMergeWarps][D];
   __shared__ float sm_f[kMergeParts], sm_l[kMergeWarps], sm_m[kMergeWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  mx_begin();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int4 hds[kMergeHeads];
 #pragma unroll
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_kernel(const MxAttn
 template <int D, int CHUNK>
 __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_rows_kernel(const MxAttnParams p) {
   constexpr int kCh = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  mx_begin();
   const int lane = threadIdx.x & 31, row = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
   const int w = blockIdx.x;
   const int4 hd = __ldcg(p.headers + w);
@@ -836,19 +836,12 @@ template <int D, int CHUNK>
 loopvq_status launch_merge(const MxAttnParams& p, int64_t rows, cudaStream_t s) {
   const int64_t units = (int64_t)p.L.batch * p.H * ((rows + CHUNK - 1) / CHUNK);
   const bool many_parts = p.n_workers > 24 * units;
-  cudaLaunchConfig_t cfg = {};
   const int most = (int)(rows < CHUNK ? rows : CHUNK);
-  cfg.gridDim = many_parts ? dim3((p.n_workers + kMergeHeads - 1) / kMergeHeads, most < 16 ? most : 16)
-                           : dim3(p.n_workers, (most + kMergeWarps - 1) / kMergeWarps);
-  cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = many_parts ? cudaLaunchKernelEx(&cfg, mx_merge_kernel<D, CHUNK>, p)
-                                   : cudaLaunchKernelEx(&cfg, mx_merge_rows_kernel<D, CHUNK>, p);
+  const cudaError_t e =
+      many_parts ? mx_launch(mx_merge_kernel<D, CHUNK>, dim3((p.n_workers + kMergeHeads - 1) / kMergeHeads, most < 16 ? most : 16),
+                             kMergeWarps * 32, 0, s, p)
+                 : mx_launch(mx_merge_rows_kernel<D, CHUNK>, dim3(p.n_workers, (most + kMergeWarps - 1) / kMergeWarps),
+                             kMergeWarps * 32, 0, s, p);
   return e == cudaSuccess ? LOOPVQ_OK : LOOPVQ_ERR_CUDA;
 }
 template <int D, int FMT, int NARROW, int TERMS, int NT>
@@ -856,8 +849,7 @@ loopvq_status launch_attn(const MxAttnParams& p, int grid, int64_t rows, cudaStr
   constexpr int smem = MxRing<D, FMT, NARROW, NT>::kBytes, W = MxRing<D, FMT, NARROW, NT>::kWarps, CHUNK = MxRows<D, NARROW>::kPerGroup * NT;
   auto kfn = mx_attn_kernel<D, FMT, NARROW, TERMS, NT>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LOOPVQ_ERR_CUDA;
-  kfn<<<grid, (W + 1) * 32, smem, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return LOOPVQ_ERR_CUDA;
+  if (mx_launch(kfn, dim3(grid), (W + 1) * 32, smem, s, p) != cudaSuccess) return LOOPVQ_ERR_CUDA;
   return launch_merge<D, CHUNK>(p, rows, s);
 }
 template <int D, int FMT>

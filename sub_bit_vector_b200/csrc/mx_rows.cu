@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
   static_assert(sizeof(RowsInfo) <= 1024 && S <= 4, "");
   RowsInfo& I = *reinterpret_cast<RowsInfo*>(sm + R::kInfo);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  mx_begin();
 
   // this block's share of the list of tiles
   int u0 = 0, t0 = 0;
@@ -679,8 +679,7 @@ cudaError_t launch(const MxAttnParams& p, int grid, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(mx_rows_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  mx_rows_kernel<D, FMT><<<grid, kRowsThreads, smem, s>>>(p);
-  return cudaGetLastError();
+  return mx_launch(mx_rows_kernel<D, FMT>, dim3(grid), kRowsThreads, smem, s, p);
 }
 
 }  // namespace
