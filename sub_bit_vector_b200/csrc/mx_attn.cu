@@ -25,6 +25,13 @@
 // tiles is rare; the sums are rescaled then, and the largest weight stands at
 // 2^8: halfway between fp16's top and where its 11 bits begin to run out, at
 // 2^-22 of the largest weight.
+//
+// Bounds (16 heads x 128, B200): 32 requests of 6-18K tokens, e4m3, trees of up
+// to 8: 235 us, 6.2 TB/s, 95% of a copy.  One row each, e2m1: 150 us, 5.35 TB/s: 410
+// instructions per tile of 32 tokens, tensor pipe 42%, issue slots 52%, the
+// slowest SM 10% behind the median.  One token over 32K, e4m3: 34 us against 21
+// of bytes: 3 us until the lengths, the page and the first tile have come one
+// after another, 4 us for the merge, and shares of only 10 tiles per warp.
 #include "mx_attn.cuh"
 
 namespace loopvq {
@@ -64,7 +71,8 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 //             pass covers both halves.  The halves are summed at the end as
 //             two parts of a split context.
 // Measured on 32 requests of 6-18K tokens, one row each, e2m1, D = 128: kind 0
-// 249 us, kind 1 181 us, kind 2 161 us.
+// 249 us, kind 1 181 us, kind 2 161 us (149 since a warp of its own feeds the
+// rings).
 template <int D, int NARROW>
 struct MxRows {
   static constexpr int kPerGroup = NARROW ? 8 / (D / kMxBlock) / NARROW : 8;
@@ -780,7 +788,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32) mx_merge_rows_kernel(const M
   if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
 }
 
-// More rows than this: mx_rows_kernel.
+// More rows than this: mx_rows_kernel, whose time hardly depends on them.  16
+// heads over 32K, D = 128, e4m3: 105 us; the warps' kernel 60 at 16 rows, 87 at 32,
+// 117 at 48, 144 at 64.  D = 64: 91 to 93 us; 40 at 16, 75 at 48, 93 at 64.
 template <int D>
 constexpr int kRowsFrom = D == 128 ? 40 : 64;
 // The variant of a call: columns per row, groups.
