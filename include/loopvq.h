@@ -673,7 +673,7 @@ LOOPVQ_API size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, con
  *   q         : device, (row, hq, d) at row*q_stride_n + hq*q_stride_h + d in
  *               q_dtype.  Query head hq reads KV head hq / (Hq / H).
  *   slopes    : device fp32 [Hq], or NULL.
- *   out       : device [total_new][Hq][D] in out_dtype; lse_out: device fp32
+ *   out       : device [total_new][Hq][D] in out_dtype, 16-byte aligned; lse_out: device fp32
  *               [total_new][Hq] natural log-sum-exp, or NULL.
  *   workspace : device, 256-byte aligned; needs no initialisation, holds
  *               nothing between calls.  Calls that may overlap on the GPU

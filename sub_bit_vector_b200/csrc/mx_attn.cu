@@ -2,14 +2,14 @@
 // microscaled KV cache.
 //
 // Rows: the query rows of a request that read one KV head, row = node * G +
-// query head in the group; a chunk is 8 * NT of them.  A unit is (request, KV
-// head, chunk); the tiles of all units form one list, and every warp of the
-// grid takes the same number of consecutive tiles of it, whatever unit they
-// belong to: ragged batches and single long contexts fill the machine alike.
-// A warp works alone: its ring of tiles is filled by TMA bulk copies that its
-// own lane 0 issues, its softmax state and sums stay in its registers, and a
-// unit that it holds whole is finished there.  A unit that spans warps leaves
-// one partial result per warp, which mx_merge_kernel adds up.
+// query head in the group; a chunk is what one warp takes together (MxRows).  A
+// unit is (request, KV head, chunk); the tiles of all units form one list, and
+// every warp of the grid takes the same number (or one more) of consecutive
+// tiles of it, whatever unit they belong to: ragged batches and single long
+// contexts fill the machine alike.  A warp computes alone: one warp of its block
+// fills its ring with TMA bulk copies, its softmax state and sums stay in its
+// registers, and a unit that it holds whole is finished there.  A unit that
+// spans warps leaves one partial result per warp; the merge kernels add them up.
 //
 // Scores: A = 16 query rows x 16 channels, B = the codes of 8 tokens as fp16
 // (exact), fp32 sums per block of 32 channels, times the block's scale in
