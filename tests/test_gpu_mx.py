@@ -760,3 +760,33 @@ def test_offsets_past_32_bits():
     q = _queries(s, "bf16")
     o, l = _run(s, q, None, lay=lay)
     _check(s, q, [ref[0]], [ref[0]], None, o, l)
+
+
+@pytest.mark.parametrize("Hq,new", [(2, [[2, 3], [3, 1], [0, 2]]), (4, [[64, 3], [40, 20], [1, 60]])])
+def test_captured_attention_replays_on_new_lengths(Hq, new):
+    """One graph, lengths and rows changed in place between its replays, within
+    the bounds that the layout gave: both kernels of rows."""
+    s = Setup([700, 900], new[0], D=64, H=1, Hq=Hq, seed=40, fmt="e2m1")
+    K, V = _filled(s)
+    rows = max(sum(n) for n in new)
+    ctx, off = _i32([700, 900]), _i32([0, 0, 0])
+    lay = L.make_mx_layout(2, s.page, s.max_pages, s.n_pages * s.page, 900, 64, rows, ctx, off, _i32(s.table.tolist()))
+    q = torch.from_numpy(s.rng.standard_normal((rows, Hq, 64)).astype(np.float32)).cuda().to(torch.bfloat16)
+    out, lse = torch.zeros((rows, Hq, 64), dtype=torch.bfloat16, device="cuda"), torch.zeros((rows, Hq), device="cuda")
+    ws = torch.full((L.loopvq_mx_attn_workspace_bytes(s.desc, lay),), 0xFF, dtype=torch.uint8, device="cuda")
+    call = L.prepare_mx_attn(s.desc, lay, s.poolK, s.poolV, q, Hq * 64, 64, None, 0, 0.125, 0.0, None, out, lse, ws, s.fault)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    s.out = "bf16"
+    for lengths, n in zip(([700, 900], [45, 333], [64, 900]), new):
+        s.ctx, s.new, s.off = lengths, n, np.concatenate([[0], np.cumsum(n)]).astype(int)
+        ctx.copy_(_i32(lengths))
+        off.copy_(_i32(s.off.tolist()))
+        out.fill_(7)
+        lse.fill_(7)
+        g.replay()
+        o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+        _check(s, q.double().cpu().numpy(), [k[:c] for k, c in zip(K, lengths)], [v[:c] for v, c in zip(V, lengths)], None, o, l)
+        assert (o[s.off[-1]:] == 7).all() and (l[s.off[-1]:] == 7).all() and s.faults() == 0
