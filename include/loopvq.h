@@ -681,12 +681,14 @@ LOOPVQ_API size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, con
  * A token that sees nothing gets a zero output and lse -inf.  What a token
  * does not see never reaches its output, whatever the pool holds there.
  * Scores are fp32 sums of exact products of codes and q (q in fp32: to 22
- * bits; elements below 2^-28 of their row's largest to 2^-38 of it); softmax
- * statistics are fp32; the weights meet the values in fp16 (11 bits) for bf16
- * q and out, and as two fp16 terms (22 bits) else.  With bf16 q and out and
- * many rows (tokens x query heads of a KV head: more than 40 for D = 128, 64
- * for D = 64) the tensor cores take keys and values to 2^-24 of 2^E, E the
- * token's largest scale exponent: exact unless its blocks are 2^15 apart.
+ * bits; elements below 2^-28 of their row's largest to 2^-38 of it).  A cap adds
+ * the relative error of tanhf; with bf16 q and out and a cap up to 64 an
+ * absolute one of 2^-22 of the cap.  Softmax statistics are fp32; the weights
+ * meet the values in fp16 (11 bits) for bf16 q and out, and as two fp16 terms
+ * (22 bits) else.  With bf16 q and out and many rows (tokens x query heads of a
+ * KV head: more than 40 for D = 128, 64 for D = 64) the tensor cores take keys
+ * and values to 2^-24 of 2^E, E the token's largest scale exponent: exact unless
+ * its blocks are 2^15 apart.
  * Results do not depend on what else runs; the same call gives the same bits.
  * Launches two kernels, of which the second adds up split contexts.
  */

@@ -388,10 +388,11 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
             }
           }
           if (p.softcap > 0.f) {
+            const bool fast = TERMS == 1 && p.softcap <= kFastCap;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-              for (int t = 0; t < 4; ++t) x[i][t] = p.softcap * kLog2e * (TERMS == 2 ? tanhf(x[i][t]) : tanh_abs(x[i][t]));
+              for (int t = 0; t < 4; ++t) x[i][t] = fast ? capped_fast(x[i][t], p.softcap) : capped(x[i][t], p.softcap);
           }
           if (p.slopes || edge) {
 #pragma unroll

@@ -33,13 +33,19 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// tanh y = 1 - 2 / (1 + e^2y), right to 2^-22 absolutely: a cap of 50 makes that 1e-5
-// of a weight, well below fp16's 2^-11 (with fp32 in or out tanhf is called).
+// tanh y = 1 - 2 / (1 + e^2y), right to 2^-22 absolutely.
 __device__ __forceinline__ float tanh_abs(float y) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(2.f * kLog2e * y)));
   return fmaf(-2.f, r, 1.f);
 }
+// A capped score in log2 units.  tanh_abs misses a score by 2^-22 of the cap,
+// however small the score is: with a cap up to kFastCap by 2^-16, 1/32 of what the
+// rounding of a weight to fp16 loses.  Above, and with fp32 in or out, tanhf,
+// whose error is relative to the score.
+constexpr float kFastCap = 64.f;
+__device__ __forceinline__ float capped_fast(float y, float cap) { return cap * kLog2e * tanh_abs(y); }
+__device__ __forceinline__ float capped(float y, float cap) { return cap * kLog2e * tanhf(y); }
 // 8 channels of a query row.
 template <typename T>
 __device__ __forceinline__ void load_query(const void* q, int64_t at, int vec, float* v) {

@@ -508,7 +508,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         }
         if (p.softcap > 0.f) {
 #pragma unroll
-          for (int t = 0; t < 32; ++t) x[t] = p.softcap * kLog2e * tanh_abs(x[t]);
+          for (int t = 0; t < 32; ++t)
+            x[t] = p.softcap <= kFastCap ? capped_fast(x[t], p.softcap) : capped(x[t], p.softcap);
         }
         if (p.slopes) {
 #pragma unroll

@@ -1,0 +1,64 @@
+"""Microscaled KV cache on the GPU where its contract ends.
+
+Bounds as in test_gpu_mx.py, whose batch and oracle helpers are used; what is
+added to the error ds of a score is derived at each test.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from test_gpu_mx import Setup, _filled, _queries, _run
+
+pytestmark = pytest.mark.gpu
+
+
+def _close(s, q, K, V, out, lse, *, cap=0.0, fine=False, scale=None, more=None, lost=None):
+    """Chains of new tokens against the oracle.  ds = (32 * 2^-24 + 2^-22) B +
+    more(qq, k) per row; lost(p, v): what an output may lose besides."""
+    scale = s.D ** -0.5 if scale is None else scale
+    cap = float(np.float32(cap))
+    G = s.Hq // s.H
+    for r, (c, n) in enumerate(zip(s.ctx, s.new)):
+        sees = np.tril(np.ones((n, c), dtype=bool), c - n)
+        for hq in range(s.Hq if n else 0):
+            k, v = K[r][:, hq // G], V[r][:, hq // G]
+            rows = slice(s.off[r], s.off[r + 1])
+            qq = q[rows, hq].astype(np.float64)
+            o, l, a, big = O.mx_attention(qq, k, v, sees, None, None, scale, cap)
+            B = np.where(sees, scale * (np.abs(qq) @ np.abs(k).T), 0).max(1)
+            ds = (32 * 2.0 ** -24 + 2.0 ** -22) * B + (0 if more is None else more(qq, k, B))
+            # two weights' scores are off by ds each: e^(2 ds) - 1, which is 2 ds where that is small
+            w = np.expm1(np.minimum(2 * ds, 50.0)) + 2.0 ** -22 + (2.0 ** -21 if fine else 2.0 ** -11) + 2.0 ** -17
+            tol = a * w[:, None] + c * 2.0 ** -32 * big + np.abs(o) * (2.0 ** -24 if s.out == "f32" else 2.0 ** -8) + 1e-37
+            if lost is not None:
+                x = np.where(sees, scale * (qq @ k.T), -np.inf)
+                p = np.exp(x - x.max(-1, keepdims=True))
+                tol = tol + lost(p / p.sum(-1, keepdims=True), v)
+            err = np.abs(out[rows, hq] - o)
+            assert (err <= tol).all(), (r, hq, float(np.max(err / tol)))
+            assert (np.abs(lse[rows, hq] - l) <= ds + 2.0 ** -18 + 2.0 ** -22 * np.abs(l)).all(), (r, hq)
+
+
+# Rows (new tokens x query heads of a KV head) that reach every form of the
+# attention: halves and blocks in columns, rows in columns, the tensor cores.
+ROWS = [(1, 1), (2, 1), (3, 1), (7, 1), (20, 1), (33, 4)]
+
+
+@pytest.mark.parametrize("cap", [1e-30, 1.0, 64.0, 65.0, 1e3, 1e4, 1e6, 1e8])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_caps_of_any_size(D, types, cap):
+    """s = cap * tanh(s / cap) for caps far below and far above the scores.  With
+    fp32 in or out, or a cap above 64, the error is relative to the score: 2^-22 of
+    tanhf and four roundings are below 2^-20 B, whatever the cap.  With bf16 in and out and a cap up to 64: 2^-22 of the cap."""
+    fine = "f32" in types
+    for n, G in ROWS:
+        s = Setup([190 + n, n + 3], [n, n], D=D, fmt="e4m3", H=1, Hq=G, seed=n + D, page=64)
+        K, V = _filled(s)
+        for gain in (1.0, 60.0):
+            q = _queries(s, types[0], gain)
+            o, l = _run(s, q, None, q_t=types[0], out_t=types[1], cap=cap)
+            _close(s, q, K, V, o, l, cap=cap, fine=fine,
+                   more=lambda qq, k, B: 2.0 ** -20 * B if fine or cap > 64 else 2.0 ** -22 * cap)
+        assert s.faults() == 0
