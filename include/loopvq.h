@@ -661,7 +661,8 @@ LOOPVQ_API size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, con
  * chain of drafted ones, whose keys and values are in the cache already) over
  * its context at one loop step.  With P = ctx_len - n_r, new token i sees the
  * prefix p < P and the new tokens j with bit j of its mask set (the scores
- * have to be finite in fp32):
+ * may not exceed 2^126 in magnitude, nor softmax_scale times an element of q
+ * 2^110):
  *   s = softmax_scale * q . k;  s = softcap * tanh(s / softcap) if softcap > 0;
  *   s = s - slopes[hq] * (pos_i - pos_n) if slopes is given;
  *   o = sum_n softmax(s)_n v_n

@@ -32,6 +32,8 @@
 // slowest SM 10% behind the median.  One token over 32K, e4m3: 34 us against 21
 // of bytes: 3 us until the lengths, the page and the first tile have come one
 // after another, 4 us for the merge, and shares of only 10 tiles per warp.
+#include <cmath>
+
 #include "mx_attn.cuh"
 
 namespace loopvq {
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
       const int ex = max((int)(__float_as_uint(mx) >> 23), 1) - 127;
       const int k2 = min(14 - ex, 120);
       const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
-      f[i] = p.softcap > 0.f ? p.scale / p.softcap * down : p.scale * kLog2e * down;
+      f[i] = p.scale * down * (p.softcap > 0.f ? 1.f : kLog2e);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
                 }
               }
             }
-          // ---- in log2 units, with cap, bias and mask: row gr of group i, tokens 4c + t
+          // ---- in log2 units (up to the cap in natural ones), with cap, bias and mask: row gr of group i, tokens 4c + t
           const int pos = tok0 + 4 * quad;
           float x[NT][4];
           uint32_t hide = 0;   // bit 4i + t: not seen
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-              for (int t = 0; t < 4; ++t) x[i][t] = fast ? capped_fast(x[i][t], p.softcap) : capped(x[i][t], p.softcap);
+              for (int t = 0; t < 4; ++t) x[i][t] = fast ? capped_fast(x[i][t], p.softcap, p.inv_cap) : capped(x[i][t], p.softcap, p.inv_cap);
           }
           if (p.slopes || edge) {
 #pragma unroll
@@ -953,6 +955,7 @@ extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq
   p.tree_mask = tree_mask;
   p.scale = softmax_scale;
   p.softcap = softcap;
+  p.inv_cap = softcap > 0.f ? std::fmin(1.f / softcap, 0x1p126f) : 0.f;   // of a smaller cap every score but 0 is at it
   p.slopes = slopes;
   p.out = out;
   p.out_bf16 = out_dtype == LOOPVQ_BF16;

@@ -16,7 +16,7 @@ struct MxAttnParams {
   int q_bf16, q_vec;
   int64_t qn, qh;
   const uint64_t* tree_mask;
-  float scale, softcap;
+  float scale, softcap, inv_cap;   // inv_cap: 1 / softcap, at most 2^126
   const float* slopes;
   void* out;
   int out_bf16;
@@ -33,19 +33,21 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// tanh y = 1 - 2 / (1 + e^2y), right to 2^-22 absolutely.
-__device__ __forceinline__ float tanh_abs(float y) {
+// tanh y = 1 - 2 / (1 + e^2y), right to 2^-22 absolutely; y2 = 2 log2(e) y.
+__device__ __forceinline__ float tanh_abs(float y2) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(2.f * kLog2e * y)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y2)));
   return fmaf(-2.f, r, 1.f);
 }
-// A capped score in log2 units.  tanh_abs misses a score by 2^-22 of the cap,
-// however small the score is: with a cap up to kFastCap by 2^-16, 1/32 of what the
+// Score s, capped, in log2 units; inv: 1 / cap.  tanh_abs misses s by 2^-22 of the
+// cap, however small s is: with a cap up to kFastCap by 2^-16, 1/32 of what the
 // rounding of a weight to fp16 loses.  Above, and with fp32 in or out, tanhf,
-// whose error is relative to the score.
+// whose error is relative to s (s / cap in steps of 2^-149, s of 2^-21 at most).
 constexpr float kFastCap = 64.f;
-__device__ __forceinline__ float capped_fast(float y, float cap) { return cap * kLog2e * tanh_abs(y); }
-__device__ __forceinline__ float capped(float y, float cap) { return cap * kLog2e * tanhf(y); }
+__device__ __forceinline__ float capped_fast(float s, float cap, float inv) {
+  return cap * kLog2e * tanh_abs(s * (2.f * kLog2e * inv));
+}
+__device__ __forceinline__ float capped(float s, float cap, float inv) { return cap * tanhf(s * inv) * kLog2e; }
 // 8 channels of a query row.
 template <typename T>
 __device__ __forceinline__ void load_query(const void* q, int64_t at, int vec, float* v) {

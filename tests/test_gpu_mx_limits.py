@@ -62,3 +62,38 @@ def test_caps_of_any_size(D, types, cap):
             _close(s, q, K, V, o, l, cap=cap, fine=fine,
                    more=lambda qq, k, B: 2.0 ** -20 * B if fine or cap > 64 else 2.0 ** -22 * cap)
         assert s.faults() == 0
+
+
+@pytest.mark.parametrize("cap", [1e-45, 3e-39, 2.0 ** 126, 3e38])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_caps_at_the_ends_of_fp32(D, types, cap):
+    """Caps whose reciprocal or whose product with log2 e is no fp32 number, and
+    queries of zeros among the others (0 times that reciprocal is 0).  A
+    reciprocal of 2^-128 in steps of 2^-149 is right to 2^-22: 2^-20 B as above.
+    s / cap itself is rounded to half a step of 2^-149: 2^-150 of the cap."""
+    fine = "f32" in types
+    for n, G in ROWS:
+        s = Setup([190 + n, n + 3], [n, n], D=D, fmt="e4m3", H=1, Hq=G, seed=n + D, page=64)
+        K, V = _filled(s)
+        q = _queries(s, types[0], 60.0)
+        q[::2] = 0
+        o, l = _run(s, q, None, q_t=types[0], out_t=types[1], cap=cap)
+        _close(s, q, K, V, o, l, cap=cap, fine=fine,
+               more=lambda qq, k, B: 2.0 ** -20 * B + 2.0 ** -150 * cap if fine or cap > 64 else 2.0 ** -22 * cap)
+        assert s.faults() == 0
+
+
+@pytest.mark.parametrize("scale,gain", [(3.0e38, 2.0 ** -127), (2.0 ** -100, 2.0 ** 97)])
+def test_softmax_scales_at_the_ends_of_fp32(scale, gain):
+    """The largest scale that is taken, and a small one, on queries that make the
+    scores ordinary again."""
+    for n, G in ROWS:
+        s = Setup([190 + n], [n], D=64, fmt="e4m3", H=1, Hq=G, seed=n, page=64)
+        K, V = _filled(s)
+        q = (_queries(s, "bf16").astype(np.float64) * gain).astype(np.float32)
+        q = torch.from_numpy(q).to(torch.bfloat16).float().numpy()
+        for cap in (0.0, 30.0, 1e6):
+            o, l = _run(s, q, None, cap=cap, scale=scale)
+            _close(s, q, K, V, o, l, cap=cap, scale=float(np.float32(scale)),
+                   more=lambda qq, k, B: 2.0 ** -20 * B + 2.0 ** -22 * min(cap, 64))
