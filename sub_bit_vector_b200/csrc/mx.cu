@@ -115,12 +115,12 @@ struct MxRaw {
         }
       }
     } else if constexpr (kWords == 2) {
-      const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+      const uint2 u = ld_once(reinterpret_cast<const uint2*>(p));
       w[0] = u.x; w[1] = u.y;
     } else {
 #pragma unroll
       for (int i = 0; i < kWords / 4; ++i) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        const uint4 u = ld_once(reinterpret_cast<const uint4*>(p) + i);
         w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
       }
     }
@@ -366,13 +366,13 @@ __global__ void __launch_bounds__(256) mx_read_kernel(const MxMoveParams p) {
     if constexpr (FMT == LOOPVQ_MX_E4M3) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint4 z = __ldg(reinterpret_cast<const uint4*>(u.tile + mx_code_off<D, FMT>(sub, b, lane)));
+        const uint4 z = ld_once(reinterpret_cast<const uint4*>(u.tile + mx_code_off<D, FMT>(sub, b, lane)));
         w[b][0] = z.x; w[b][1] = z.y; w[b][2] = z.z; w[b][3] = z.w;
       }
     } else {
 #pragma unroll
       for (int b = 0; b < NB; b += 2) {
-        const uint4 z = __ldg(reinterpret_cast<const uint4*>(u.tile + mx_code_off<D, FMT>(sub, b, lane)));
+        const uint4 z = ld_once(reinterpret_cast<const uint4*>(u.tile + mx_code_off<D, FMT>(sub, b, lane)));
         w[b][0] = z.x; w[b][1] = z.y; w[b + 1][0] = z.z; w[b + 1][1] = z.w;
       }
     }
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeep
   mx_begin();
   const MxFew<D> u(p.L, p.H, p.fault);
   if (!u.there) return;
-  const int r = blockIdx.z, nk = __ldg(p.n_keep + r);
+  const int r = blockIdx.z, nk = ld_once(p.n_keep + r);
   if (nk < 0 || nk > u.q.n || nk > p.max_keep || nk > p.room) {
     set_fault(p.fault, LOOPVQ_FAULT_CTX_RANGE);
     return;
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kMxKeepWarps * 32) mx_keep_kernel(const MxKeep
     const int i = lane + 32 * k;
     from[k] = -1;
     if (i < nk) {
-      const int f = __ldg(p.keep + (int64_t)r * p.max_keep + i);
+      const int f = ld_once(p.keep + (int64_t)r * p.max_keep + i);
       if (f < 0 || f >= u.q.n) set_fault(p.fault, LOOPVQ_FAULT_CTX_RANGE);
       else if (f != i && tile_of(u.q.base + f) >= 0) from[k] = f;
     }

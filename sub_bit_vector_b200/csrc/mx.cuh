@@ -39,6 +39,37 @@ inline size_t mx_tile_bytes(int D, int fmt) {
   return (size_t)kMxTile * D * (fmt == LOOPVQ_MX_E4M3 ? 8 : 4) / 8 + (size_t)kMxTile * (D / kMxBlock);
 }
 
+// Loads of what an earlier kernel of the stream may have written, the caller's
+// arrays among it.  A kernel may be resident while that kernel still runs
+// (mx_begin), so the read-only path, for data that nothing writes while the kernel
+// lives, is not for them.  Each load is done once: a checked index stays the one
+// that was checked.
+__device__ __forceinline__ int32_t ld_once(const int32_t* p) {
+  int32_t v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_once(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_once(const uint64_t* p) {
+  uint64_t v;
+  asm volatile("ld.global.u64 %0, [%1];" : "=l"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_once(const uint2* p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 struct MxLayout {
   int batch, page_tokens, max_pages, max_ctx, max_new, total_new;
   int64_t n_pages;      // whole pages of the pool
@@ -51,7 +82,7 @@ struct MxReq {
 };
 // Request r's lengths; false (and the fault bit) if they are out of bounds.
 __device__ __forceinline__ bool mx_request(const MxLayout& L, int r, MxReq* q, uint32_t* fault) {
-  const int ctx = __ldg(L.ctx_len + r), a = __ldg(L.new_off + r), b = __ldg(L.new_off + r + 1);
+  const int ctx = ld_once(L.ctx_len + r), a = ld_once(L.new_off + r), b = ld_once(L.new_off + r + 1);
   const bool ok = a >= 0 && b >= a && b <= L.total_new && b - a <= L.max_new && ctx >= b - a && ctx <= L.max_ctx;
   if (!ok) {
     set_fault(fault, LOOPVQ_FAULT_CTX_RANGE);
@@ -67,7 +98,7 @@ __device__ __forceinline__ bool mx_request(const MxLayout& L, int r, MxReq* q, u
 // bit) for a page id outside the pool.  The caller has 32t < ctx_len.
 __device__ __forceinline__ int64_t mx_pool_tile(const MxLayout& L, int r, int t, uint32_t* fault) {
   const int per = L.page_tokens / kMxTile;
-  const int id = __ldg(L.pages + (int64_t)r * L.max_pages + t / per);
+  const int id = ld_once(L.pages + (int64_t)r * L.max_pages + t / per);
   if (id < 0 || id >= L.n_pages) {
     set_fault(fault, LOOPVQ_FAULT_POOL_RANGE);
     return -1;

@@ -145,7 +145,7 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
     int page = pc.t / per, in_page = pc.t % per, slot = 0;
     uint32_t phase = 1, idle = 0;   // a wait for the phase before the first does not block
     int64_t head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
-    int id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+    int id = ld_once(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
     const uint32_t ring = smem_u32(sm_ring) + lane * S * Ring::kSlot;
     for (int i = 0; i < n;) {
       if (!mbar_test(smem_u32(&empty[lane][slot]), phase)) {
@@ -177,11 +177,11 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
         mx_next_unit<CHUNK>(p, &pc);
         page = in_page = 0;
         head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
-        id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages);
+        id = ld_once(p.L.pages + (int64_t)pc.r * p.L.max_pages);
       } else if (++in_page == per) {
         in_page = 0;
         ++page;
-        id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+        id = ld_once(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
       }
     }
     return;
@@ -219,9 +219,9 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
           if (p.q_bf16) load_query<__nv_bfloat16>(p.q, at + 32 * b, p.q_vec, v[i][b]);
           else load_query<float>(p.q, at + 32 * b, p.q_vec, v[i][b]);
         }
-        sees[i] = (p.tree_mask ? __ldg(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
+        sees[i] = (p.tree_mask ? ld_once(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
         pos_q[i] = rq.base + __popcll(sees[i] & ~(1ull << node));
-        if (p.slopes) slope[i] = __ldg(p.slopes + hq) * kLog2e;
+        if (p.slopes) slope[i] = ld_once(p.slopes + hq) * kLog2e;
       }
     }
     // scaled by a power of two (NARROW: of each block) to a largest magnitude in
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
               const int j = pos + t - rq.base;   // >= 0: a new token
               int at = pos + t;
               if (p.slopes && j >= 0 && j < rq.n) {
-                const uint64_t its = p.tree_mask ? __ldg(p.tree_mask + rq.row0 + j) & all_new : (2ull << j) - 1;
+                const uint64_t its = p.tree_mask ? ld_once(p.tree_mask + rq.row0 + j) & all_new : (2ull << j) - 1;
                 at = rq.base + __popcll(its & ~(1ull << j));
               }
 #pragma unroll

@@ -60,7 +60,7 @@ __device__ __forceinline__ void load_query(const void* q, int64_t at, int vec, f
   __align__(16) uint32_t w[sizeof(T) * 2];
 #pragma unroll
   for (int k = 0; k < (int)sizeof(T) / 2; ++k)
-    reinterpret_cast<uint4*>(w)[k] = __ldg(reinterpret_cast<const uint4*>(x) + k);
+    reinterpret_cast<uint4*>(w)[k] = ld_once(reinterpret_cast<const uint4*>(x) + k);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     v[k] = sizeof(T) == 4 ? __uint_as_float(w[k % (sizeof(T) * 2)]) : k & 1 ? bf16_hi(w[k / 2]) : bf16_lo(w[k / 2]);

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
           const int j = tok0 + lane - rq.base;
           int at = tok0 + lane;
           if (j >= 0 && j < rq.n) {
-            const uint64_t its = p.tree_mask ? __ldg(p.tree_mask + rq.row0 + j) & all_new : (2ull << j) - 1;
+            const uint64_t its = p.tree_mask ? ld_once(p.tree_mask + rq.row0 + j) & all_new : (2ull << j) - 1;
             at = rq.base + __popcll(its & ~(1ull << j));
           }
           T.pos[lane] = at;
@@ -415,18 +415,18 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
           mx_next_unit<CHUNK>(p, &pc);
           page = in_page = 0;
           head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
-          id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages);
+          id = ld_once(p.L.pages + (int64_t)pc.r * p.L.max_pages);
         } else if (++in_page == per) {
           in_page = 0;
           ++page;
-          id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+          id = ld_once(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
         }
       }
     };
     const bool copier = tid == 96;
     if (copier) {
       head = (int64_t)(pc.u / (pc.units / p.H)) * p.L.pool_tiles;
-      id = __ldg(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
+      id = ld_once(p.L.pages + (int64_t)pc.r * p.L.max_pages + page);
       for (int i = 0; i < S && i < count; ++i) issue(i);
     }
     int slot = 0;
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
           if (p.q_vec) {
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) {
-              const uint4 z = __ldg(reinterpret_cast<const uint4*>(x) + k);
+              const uint4 z = ld_once(reinterpret_cast<const uint4*>(x) + k);
               q[4 * k] = z.x; q[4 * k + 1] = z.y; q[4 * k + 2] = z.z; q[4 * k + 3] = z.w;
             }
           } else {
@@ -466,9 +466,9 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
 #pragma unroll
             for (int k = 0; k < D / 2; ++k) q[k] = (uint32_t)x16[2 * k] | (uint32_t)x16[2 * k + 1] << 16;
           }
-          sees = (p.tree_mask ? __ldg(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
+          sees = (p.tree_mask ? ld_once(p.tree_mask + rq.row0 + node) : (2ull << node) - 1) & all_new;
           pos_q = rq.base + __popcll(sees & ~(1ull << node));
-          if (p.slopes) slope = __ldg(p.slopes + hq) * kLog2e;
+          if (p.slopes) slope = ld_once(p.slopes + hq) * kLog2e;
         }
 #pragma unroll
         for (int k = 0; k < D / 2; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(q[k])), fabsf(bf16_hi(q[k]))));

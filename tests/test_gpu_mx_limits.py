@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import oracle as O
-from test_gpu_mx import Setup, _filled, _queries, _run
+from sub_bit_vector_b200 import loopvq as L
+from test_gpu_mx import Setup, _filled, _i32, _queries, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +98,44 @@ def test_softmax_scales_at_the_ends_of_fp32(scale, gain):
             o, l = _run(s, q, None, cap=cap, scale=scale)
             _close(s, q, K, V, o, l, cap=cap, scale=float(np.float32(scale)),
                    more=lambda qq, k, B: 2.0 ** -20 * B + 2.0 ** -22 * min(cap, 64))
+
+
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+def test_kernels_that_follow_closely_see_the_last_ones_bytes(fmt, new):
+    """Write, keep, read and attend again and again in one stream with no host wait
+    between them, each input made by the operation before it: every result is
+    what the calls give one at a time."""
+    s = Setup([300, 190 + new, new], [new, new, new], D=128, fmt=fmt, H=4, Hq=8, page=64, seed=new)
+    _filled(s)
+    first = s.poolK.clone(), s.poolV.clone()
+    x = torch.from_numpy(s.rng.standard_normal((2, s.rows, s.H, s.D)).astype(np.float32)).cuda().to(torch.bfloat16)
+    keep, n_keep = _i32([[new - 1], [0], [new // 2]]), _i32([1, 1, 1])
+    ws = torch.zeros(L.loopvq_mx_attn_workspace_bytes(s.desc, s.lay), dtype=torch.uint8, device="cuda")
+
+    def go(wait):
+        s.poolK.copy_(first[0])
+        s.poolV.copy_(first[1])
+        a, res = x.clone(), []
+        for i in range(40):
+            a = a * -1.25 if i % 3 else a * 0.5 + 1        # a torch kernel writes the rows
+            wait()
+            L.loopvq_mx_write(s.desc, s.lay, 0, 1, a[0], a[1], 0, s.H * s.D, s.D, s.poolK, s.poolV, s.fault)
+            wait()
+            k, v = torch.empty_like(a[0:1]), torch.empty_like(a[0:1])
+            L.loopvq_mx_read(s.desc, s.lay, 0, 1, s.poolK, s.poolV, k, v, 0, s.H * s.D, s.D, s.fault)
+            wait()
+            L.loopvq_mx_keep(s.desc, s.lay, keep, n_keep, 1, s.poolK, s.poolV, s.fault)
+            wait()
+            out = torch.empty((s.rows, s.Hq, s.D), dtype=torch.bfloat16, device="cuda")
+            L.loopvq_mx_attn(s.desc, s.lay, s.poolK, s.poolV, torch.cat([k[0], v[0]], 1), 8 * s.D, s.D, None, 0, 0.02, 0.0,
+                             None, out, None, ws, s.fault)
+            wait()
+            a = torch.stack([out[:, :s.H], out[:, s.H:]])  # the next rows come from this output
+            res += [k, v, out]
+        torch.cuda.synchronize()
+        return res
+
+    for a, b in zip(go(torch.cuda.synchronize), go(lambda: None)):
+        assert torch.equal(a, b)
+    assert s.faults() == 0
