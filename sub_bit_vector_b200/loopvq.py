@@ -390,6 +390,13 @@ def _mx_pools(desc, layout, poolK, poolV) -> None:
     _want("poolV", poolV, ("uint8",), n)
 
 
+def _mx_buffers(desc, layout, poolK, poolV, fault_bits) -> None:
+    """What every call has: the layout's arrays, both pools and the fault word."""
+    _here(poolK, poolV, fault_bits, *layout._keep)
+    _mx_pools(desc, layout, poolK, poolV)
+    _want("fault_bits", fault_bits, ("int32", "uint32"), 1)
+
+
 def _mx_rows(desc, layout, first_step, n_steps, a, b, stride_t, stride_n, stride_h) -> None:
     if a.dtype != b.dtype:
         raise TypeError("k and v differ in type")
@@ -432,8 +439,8 @@ def prepare_mx_write(desc, layout, first_step, n_steps, k, v, stride_t, stride_n
     returns a zero-argument callable that issues the call, without a stream on
     the one that is current then.  The tensors must stay in place; their
     contents may change between calls."""
-    _here(k, v, poolK, poolV, *layout._keep)
-    _mx_pools(desc, layout, poolK, poolV)
+    _here(k, v)
+    _mx_buffers(desc, layout, poolK, poolV, fault_bits)
     _mx_rows(desc, layout, first_step, n_steps, k, v, stride_t, stride_n, stride_h)
     return _prepared("loopvq_mx_write", (
         ctypes.byref(desc), ctypes.byref(layout), first_step, n_steps, _ptr(k), _ptr(v), _dtype_code(k), stride_t,
@@ -452,8 +459,8 @@ def loopvq_mx_write(desc, layout, first_step, n_steps, k, v, stride_t, stride_n,
 def prepare_mx_read(desc, layout, first_step, n_steps, poolK, poolV, k_out, v_out, stride_t, stride_n, stride_h,
                     fault_bits=None, stream=None):
     """loopvq_mx_read, prepared as prepare_mx_write is."""
-    _here(k_out, v_out, poolK, poolV, *layout._keep)
-    _mx_pools(desc, layout, poolK, poolV)
+    _here(k_out, v_out)
+    _mx_buffers(desc, layout, poolK, poolV, fault_bits)
     _mx_rows(desc, layout, first_step, n_steps, k_out, v_out, stride_t, stride_n, stride_h)
     return _prepared("loopvq_mx_read", (
         ctypes.byref(desc), ctypes.byref(layout), first_step, n_steps, _ptr(poolK), _ptr(poolV), _ptr(k_out),
@@ -476,8 +483,8 @@ def prepare_mx_attn(desc, layout, poolK, poolV, q, q_stride_n, q_stride_h, tree_
                     softcap, slopes, out, lse_out, workspace, fault_bits=None, stream=None):
     """loopvq_mx_attn, prepared as prepare_mx_write is.  tree_mask: int64 or
     uint64 [total_new], bit j of row i: new token i sees new token j."""
-    _here(q, out, lse_out, workspace, poolK, poolV, tree_mask, slopes, *layout._keep)
-    _mx_pools(desc, layout, poolK, poolV)
+    _here(q, out, lse_out, workspace, tree_mask, slopes)
+    _mx_buffers(desc, layout, poolK, poolV, fault_bits)
     rows, Hq, D = max(0, layout.total_new), desc.n_heads_q, desc.head_dim
     _want("tree_mask", tree_mask, ("int64", "uint64"), rows)
     _want("slopes", slopes, ("float32",), Hq)
@@ -502,8 +509,8 @@ def loopvq_mx_attn(desc, layout, poolK, poolV, q, q_stride_n, q_stride_h, tree_m
 
 def prepare_mx_keep(desc, layout, keep, n_keep, max_keep, poolK, poolV, fault_bits=None, stream=None):
     """loopvq_mx_keep, prepared as prepare_mx_write is."""
-    _here(keep, n_keep, poolK, poolV, *layout._keep)
-    _mx_pools(desc, layout, poolK, poolV)
+    _here(keep, n_keep)
+    _mx_buffers(desc, layout, poolK, poolV, fault_bits)
     _want("keep", keep, ("int32",), layout.batch * max(0, max_keep))
     _want("n_keep", n_keep, ("int32",), layout.batch)
     return _prepared("loopvq_mx_keep", (

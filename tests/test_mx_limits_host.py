@@ -4,6 +4,12 @@ import glob
 import os
 import re
 
+import pytest
+import torch
+
+from sub_bit_vector_b200 import loopvq as L
+from test_mx_host import FAKE, _desc, _lay
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sub_bit_vector_b200", "csrc")
 
 
@@ -19,3 +25,48 @@ def test_no_read_only_loads_in_kernels_that_start_early():
         assert "griddepcontrol.wait" in code or "mx_begin()" in code or f.endswith("mx_attn.cuh")
         for word in ("__ldg(", ".nc", "__restrict__", "ldg("):
             assert word not in code, (os.path.basename(f), word)
+
+
+# ------------------------------------------------------------------ the binding
+
+X = torch.zeros((8, 4, 128), dtype=torch.bfloat16)      # host memory: no call here reaches a launch
+
+
+def _prepare(name, **kw):
+    """prepare_mx_* with valid arguments but for kw."""
+    d, lay = kw.pop("desc", _desc()), kw.pop("lay", _lay())
+    a = dict(fault_bits=None, workspace=torch.zeros(1 << 20, dtype=torch.uint8), loop_step=0)
+    a.update(kw)
+    f = a["fault_bits"]
+    if name == "write":
+        return L.prepare_mx_write(d, lay, a["loop_step"], 1, X, X, 0, 512, 128, FAKE, FAKE, f)
+    if name == "read":
+        return L.prepare_mx_read(d, lay, a["loop_step"], 1, FAKE, FAKE, X, X, 0, 512, 128, f)
+    if name == "attn":
+        return L.prepare_mx_attn(d, lay, FAKE, FAKE, X, 512, 128, None, a["loop_step"], 0.1, 0.0, None, X, None,
+                                 a["workspace"], f)
+    return L.prepare_mx_keep(d, lay, FAKE, FAKE, 4, FAKE, FAKE, f)
+
+
+CALLS = ["write", "read", "attn", "keep"]
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_fault_words_are_checked(name, monkeypatch):
+    """The kernels write the fault word by its address: one on the host, of
+    another type or of no elements is refused before any launch."""
+    seen = []
+    here = L._here
+    with monkeypatch.context() as m:     # the other arguments of this test are in host memory too
+        m.setattr(L, "_here", lambda *t: seen.extend(t))
+        word = torch.zeros(1, dtype=torch.int32)
+        try:
+            _prepare(name, fault_bits=word)
+        except RuntimeError:             # without a GPU, at the current device: all checks have passed
+            pass
+        assert any(t is word for t in seen)
+        for bad, error in ((torch.zeros(1, dtype=torch.int64), TypeError), (torch.zeros(0, dtype=torch.int32), ValueError)):
+            with pytest.raises(error, match="fault_bits"):
+                _prepare(name, fault_bits=bad)
+    with pytest.raises(ValueError, match="not on a CUDA device"):
+        here(torch.zeros(1, dtype=torch.int32))
