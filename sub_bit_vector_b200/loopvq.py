@@ -490,6 +490,8 @@ def prepare_mx_attn(desc, layout, poolK, poolV, q, q_stride_n, q_stride_h, tree_
     _want("slopes", slopes, ("float32",), Hq)
     _want("out", out, ("float32", "bfloat16"), rows * Hq * D)
     _want("lse_out", lse_out, ("float32",), rows * Hq)
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace: consecutive bytes are needed")
     if rows and q_stride_n >= 0 and q_stride_h >= 0:
         _want_strided("q", q, (rows - 1) * q_stride_n + (Hq - 1) * q_stride_h + D - 1)
     return _prepared("loopvq_mx_attn", (

@@ -70,3 +70,10 @@ def test_fault_words_are_checked(name, monkeypatch):
                 _prepare(name, fault_bits=bad)
     with pytest.raises(ValueError, match="not on a CUDA device"):
         here(torch.zeros(1, dtype=torch.int32))
+
+
+def test_workspaces_are_consecutive(monkeypatch):
+    """A workspace's size is taken from its number of elements."""
+    monkeypatch.setattr(L, "_here", lambda *t: None)
+    with pytest.raises(ValueError, match="workspace"):
+        _prepare("attn", workspace=torch.zeros((1 << 10, 1 << 10), dtype=torch.uint8)[:, ::2])
