@@ -392,7 +392,7 @@ def _mx_pools(desc, layout, poolK, poolV) -> None:
 
 def _mx_buffers(desc, layout, poolK, poolV, fault_bits) -> None:
     """What every call has: the layout's arrays, both pools and the fault word."""
-    _here(poolK, poolV, fault_bits, *layout._keep)
+    _here(poolK, poolV, fault_bits, *getattr(layout, "_keep", ()))   # a layout made by hand holds raw addresses
     _mx_pools(desc, layout, poolK, poolV)
     _want("fault_bits", fault_bits, ("int32", "uint32"), 1)
 

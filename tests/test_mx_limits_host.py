@@ -77,3 +77,12 @@ def test_workspaces_are_consecutive(monkeypatch):
     monkeypatch.setattr(L, "_here", lambda *t: None)
     with pytest.raises(ValueError, match="workspace"):
         _prepare("attn", workspace=torch.zeros((1 << 10, 1 << 10), dtype=torch.uint8)[:, ::2])
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_layouts_made_by_hand_are_taken(name, monkeypatch):
+    """The exported structure, filled with raw addresses, without make_mx_layout."""
+    monkeypatch.setattr(L, "_here", lambda *t: None)
+    monkeypatch.setattr(L, "_prepared", lambda name, args, keep, stream: "prepared")
+    lay = L.loopvq_mx_layout(2, 64, 4, 256, 4, 8, 512, FAKE, FAKE, FAKE)
+    assert _prepare(name, lay=lay) == "prepared"
