@@ -614,7 +614,7 @@ typedef struct {
   int32_t batch;             /* 1 .. 65535 */
   int32_t page_tokens;       /* a positive multiple of 32 */
   int32_t max_pages;         /* row length of pages */
-  int32_t max_ctx_len;       /* host bound on ctx_len[r]; <= max_pages * page_tokens */
+  int32_t max_ctx_len;       /* host bound on ctx_len[r]; <= max_pages * page_tokens, 2^31 - 129 */
   int32_t max_new;           /* host bound on n_r */
   int32_t total_new;         /* rows of the packed arguments; new_off[batch] <= total_new */
   int64_t pool_tokens;       /* a positive multiple of 32 */

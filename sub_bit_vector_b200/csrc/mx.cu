@@ -754,6 +754,7 @@ loopvq_status mx_check_layout(const loopvq_mx_layout* l, MxLayout* o) {
       l->pool_tokens % kMxTile)
     return LOOPVQ_ERR_INVALID_ARG;
   if (l->max_ctx_len > (int64_t)l->max_pages * l->page_tokens) return LOOPVQ_ERR_INVALID_ARG;
+  if (l->max_ctx_len > kMxMaxContext) return LOOPVQ_ERR_UNSUPPORTED;
   if (!l->pages || !l->ctx_len || !l->new_off) return LOOPVQ_ERR_INVALID_ARG;
   if (((uintptr_t)l->pages | (uintptr_t)l->ctx_len | (uintptr_t)l->new_off) & 3) return LOOPVQ_ERR_INVALID_ARG;
   o->batch = l->batch;

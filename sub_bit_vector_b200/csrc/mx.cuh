@@ -11,6 +11,7 @@ namespace loopvq {
 constexpr int kMxTile = 32;    // tokens of a tile
 constexpr int kMxBlock = 32;   // channels that share a scale
 constexpr int kMxMaxTree = 64; // new tokens a request may have in attention and keep
+constexpr int kMxMaxContext = 0x7fffffff - 128;   // positions up to three tiles past a context's last stay ints
 constexpr int kMxExpMin = -64, kMxExpMax = 56;
 constexpr uint32_t kMxNan = 255;
 

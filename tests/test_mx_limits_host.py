@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from sub_bit_vector_b200 import loopvq as L
-from test_mx_host import FAKE, _desc, _lay
+from test_mx_host import FAKE, UNSUP, _attn, _desc, _keep, _lay, _read, _write
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sub_bit_vector_b200", "csrc")
 
@@ -86,3 +86,14 @@ def test_layouts_made_by_hand_are_taken(name, monkeypatch):
     monkeypatch.setattr(L, "_prepared", lambda name, args, keep, stream: "prepared")
     lay = L.loopvq_mx_layout(2, 64, 4, 256, 4, 8, 512, FAKE, FAKE, FAKE)
     assert _prepare(name, lay=lay) == "prepared"
+
+
+# ------------------------------------------------------- the ends of integers
+
+@pytest.mark.parametrize("call", [_write, _read, _attn, _keep])
+def test_contexts_whose_positions_pass_31_bits_refused(call):
+    """The kernels look up to three tiles past a context's last token, in ints."""
+    lay = dict(page_tokens=1 << 20, max_pages=1 << 11, pool_tokens=1 << 31)
+    for length in (2 ** 31 - 1, 2 ** 31 - 128):
+        assert call(_desc(), _lay(max_ctx_len=length, **lay)) == UNSUP
+    assert call(_desc(), _lay(max_ctx_len=2 ** 31 - 129, total_new=0, **lay)) == L.LOOPVQ_OK
