@@ -623,7 +623,8 @@ typedef struct {
   const int32_t* new_off;    /* device [batch + 1] */
 } loopvq_mx_layout;
 
-/* Bytes of one pool (K or V, all loop steps); 0 if desc or pool_tokens is invalid. */
+/* Bytes of one pool (K or V, all loop steps); 0 if desc or pool_tokens is invalid
+ * or they are 2^63 or more, which every call refuses. */
 LOOPVQ_API size_t loopvq_mx_pool_bytes(const loopvq_mx_desc* desc, int64_t pool_tokens);
 
 /*

@@ -706,6 +706,7 @@ loopvq_status move_setup(const loopvq_mx_desc* desc, const loopvq_mx_layout* lay
   if (s != LOOPVQ_OK) return s;
   s = mx_check_layout(layout, &p->L);
   if (s != LOOPVQ_OK) return s;
+  if (mx_pool_bytes(desc, layout->pool_tokens) == 0) return LOOPVQ_ERR_UNSUPPORTED;
   if (first_step < 0 || n_steps < 1 || n_steps > desc->n_loop - first_step) return LOOPVQ_ERR_INVALID_ARG;
   if (dtype != LOOPVQ_F32 && dtype != LOOPVQ_BF16) return LOOPVQ_ERR_INVALID_ARG;
   if (st < 0 || sn < 0 || sh < 0) return LOOPVQ_ERR_INVALID_ARG;
@@ -746,6 +747,12 @@ loopvq_status mx_check_desc(const loopvq_mx_desc* d) {
   if (d->head_dim != 64 && d->head_dim != 128) return LOOPVQ_ERR_UNSUPPORTED;
   if (d->n_heads_kv > 65535 || d->n_heads_q > 65535) return LOOPVQ_ERR_UNSUPPORTED;
   return LOOPVQ_OK;
+}
+
+size_t mx_pool_bytes(const loopvq_mx_desc* d, int64_t pool_tokens) {
+  const unsigned __int128 n = (unsigned __int128)d->n_loop * d->n_heads_kv * (uint64_t)(pool_tokens / kMxTile) *
+                              mx_tile_bytes(d->head_dim, d->format);
+  return n < ((unsigned __int128)1 << 63) ? (size_t)n : 0;
 }
 
 loopvq_status mx_check_layout(const loopvq_mx_layout* l, MxLayout* o) {
@@ -798,8 +805,7 @@ using namespace loopvq;
 
 extern "C" size_t loopvq_mx_pool_bytes(const loopvq_mx_desc* desc, int64_t pool_tokens) {
   if (mx_check_desc(desc) != LOOPVQ_OK || pool_tokens < kMxTile || pool_tokens % kMxTile) return 0;
-  return (size_t)desc->n_loop * desc->n_heads_kv * (size_t)(pool_tokens / kMxTile) *
-         mx_tile_bytes(desc->head_dim, desc->format);
+  return mx_pool_bytes(desc, pool_tokens);
 }
 
 extern "C" loopvq_status loopvq_mx_write(const loopvq_mx_desc* desc, const loopvq_mx_layout* layout,
@@ -856,6 +862,7 @@ extern "C" loopvq_status loopvq_mx_keep(const loopvq_mx_desc* desc, const loopvq
   if (st != LOOPVQ_OK) return st;
   st = mx_check_layout(layout, &p.L);
   if (st != LOOPVQ_OK) return st;
+  if (mx_pool_bytes(desc, layout->pool_tokens) == 0) return LOOPVQ_ERR_UNSUPPORTED;
   if (!keep || !n_keep || max_keep < 1 || ((uintptr_t)keep & 3) || ((uintptr_t)n_keep & 3)) return LOOPVQ_ERR_INVALID_ARG;
   if (!poolK || !poolV || ((uintptr_t)poolK & 15) || ((uintptr_t)poolV & 15) || ((uintptr_t)fault_bits & 3))
     return LOOPVQ_ERR_INVALID_ARG;

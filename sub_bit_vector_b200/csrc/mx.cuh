@@ -132,5 +132,7 @@ cudaError_t mx_launch(K kernel, dim3 grid, unsigned threads, size_t smem, cudaSt
 // Host checks shared by the entry points.
 loopvq_status mx_check_desc(const loopvq_mx_desc* d);
 loopvq_status mx_check_layout(const loopvq_mx_layout* l, MxLayout* out);
+// Bytes of a pool of a checked descriptor; 0 if offsets into it would pass 63 bits.
+size_t mx_pool_bytes(const loopvq_mx_desc* d, int64_t pool_tokens);
 
 }  // namespace loopvq

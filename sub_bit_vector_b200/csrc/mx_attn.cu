@@ -922,6 +922,7 @@ extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq
   MxAttnParams p = {};
   const loopvq_status st = attn_checks(desc, layout, &p.L);
   if (st != LOOPVQ_OK) return st;
+  if (mx_pool_bytes(desc, layout->pool_tokens) == 0) return LOOPVQ_ERR_UNSUPPORTED;
   if (loop_step < 0 || loop_step >= desc->n_loop) return LOOPVQ_ERR_INVALID_ARG;
   if (!poolK || !poolV || ((uintptr_t)poolK & 15) || ((uintptr_t)poolV & 15)) return LOOPVQ_ERR_INVALID_ARG;
   if ((q_dtype != LOOPVQ_F32 && q_dtype != LOOPVQ_BF16) || (out_dtype != LOOPVQ_F32 && out_dtype != LOOPVQ_BF16))

@@ -97,3 +97,14 @@ def test_contexts_whose_positions_pass_31_bits_refused(call):
     for length in (2 ** 31 - 1, 2 ** 31 - 128):
         assert call(_desc(), _lay(max_ctx_len=length, **lay)) == UNSUP
     assert call(_desc(), _lay(max_ctx_len=2 ** 31 - 129, total_new=0, **lay)) == L.LOOPVQ_OK
+
+
+@pytest.mark.parametrize("call", [_write, _read, _attn, _keep])
+def test_pools_whose_bytes_pass_63_bits_refused(call):
+    """2 steps x 2 heads x 132 bytes a token: a size that wraps to a few bytes
+    would let a small pool pass for a large one."""
+    for tokens in (1 << 56, (1 << 59) + 32, (1 << 62)):
+        assert L.loopvq_mx_pool_bytes(_desc(), tokens) == 0
+        assert call(_desc(), _lay(pool_tokens=tokens)) == UNSUP
+    assert L.loopvq_mx_pool_bytes(_desc(), 1 << 53) == (1 << 55) * 132
+    assert call(_desc(), _lay(pool_tokens=1 << 53, total_new=0)) == L.LOOPVQ_OK
