@@ -339,16 +339,28 @@ def loopvq_residual_decode_attn(desc, batch, max_ctx_len, ctx_len, tok_off, pool
 
 # ------------------------------------------------- microscaled KV cache
 
+def _fits(c_type, value, name="argument"):
+    """ctypes drops the bits of an integer that its type has no room for."""
+    if isinstance(value, int) and c_type(value).value != value:
+        raise OverflowError(f"{name}: {value} does not fit in {8 * ctypes.sizeof(c_type)} bits")
+    return value
+
+
+def _filled(struct, *values):
+    return struct(*(_fits(t, v, name) if t in (ctypes.c_int32, ctypes.c_int64) else v
+                    for (name, t), v in zip(struct._fields_, values)))
+
+
 def make_mx_desc(n_loop, n_heads_kv, head_dim, format, n_heads_q=None) -> loopvq_mx_desc:
-    return loopvq_mx_desc(n_loop, n_heads_kv, n_heads_q or n_heads_kv, head_dim, format)
+    return _filled(loopvq_mx_desc, n_loop, n_heads_kv, n_heads_q or n_heads_kv, head_dim, format)
 
 
 def make_mx_layout(batch, page_tokens, max_pages, pool_tokens, max_ctx_len, max_new, total_new, ctx_len, new_off,
                    pages) -> loopvq_mx_layout:
     for name, t, n in (("ctx_len", ctx_len, batch), ("new_off", new_off, batch + 1), ("pages", pages, batch * max_pages)):
         _want(name, t, ("int32",), n)
-    lay = loopvq_mx_layout(batch, page_tokens, max_pages, max_ctx_len, max_new, total_new, pool_tokens, _ptr(pages),
-                           _ptr(ctx_len), _ptr(new_off))
+    lay = _filled(loopvq_mx_layout, batch, page_tokens, max_pages, max_ctx_len, max_new, total_new, pool_tokens,
+                  _ptr(pages), _ptr(ctx_len), _ptr(new_off))
     lay._keep = (ctx_len, new_off, pages)
     return lay
 
@@ -413,7 +425,9 @@ def _prepared(name, args, keep, stream):
     import torch
     fn = getattr(_lib, name)
     plain = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t)
-    args = tuple(t(a) if t in plain else a for t, a in zip(fn.argtypes, args))     # converted once
+    whole = (ctypes.c_int32, ctypes.c_int64)
+    args = tuple(t(_fits(t, a) if t in whole else a) if t in plain else a
+                 for t, a in zip(fn.argtypes, args))     # converted once
     # the current stream of the buffers' device: a tenth of the cost of torch.cuda.current_stream()
     current, here = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     device = here()

@@ -108,3 +108,22 @@ def test_pools_whose_bytes_pass_63_bits_refused(call):
         assert call(_desc(), _lay(pool_tokens=tokens)) == UNSUP
     assert L.loopvq_mx_pool_bytes(_desc(), 1 << 53) == (1 << 55) * 132
     assert call(_desc(), _lay(pool_tokens=1 << 53, total_new=0)) == L.LOOPVQ_OK
+
+
+@pytest.mark.parametrize("name", ["batch", "page_tokens", "max_pages", "max_ctx_len", "max_new", "total_new"])
+def test_layout_numbers_that_do_not_fit_refused(name):
+    """2^32 tokens would have become 0, and the call one that does nothing."""
+    with pytest.raises(OverflowError, match=name):
+        _lay(**{name: 1 << 32})
+
+
+def test_numbers_that_do_not_fit_refused(monkeypatch):
+    with pytest.raises(OverflowError, match="n_loop"):
+        _desc(n_loop=(1 << 32) + 1)
+    with pytest.raises(OverflowError, match="pool_tokens"):
+        _lay(pool_tokens=1 << 64)
+    monkeypatch.setattr(L, "_here", lambda *t: None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    for name in ("write", "read", "attn"):
+        with pytest.raises(OverflowError):
+            _prepare(name, loop_step=1 << 32)
