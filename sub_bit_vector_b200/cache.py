@@ -432,6 +432,7 @@ class MXCache:
     def truncate(self, r, ctx_len) -> None:
         """Request r's context ends at ctx_len; its pages behind that are free
         (0: the request is over).  Ends the present step."""
+        r = range(self.batch)[r]
         if not 0 <= ctx_len <= self.ctx[r]:
             raise ValueError("truncate cannot grow a context")
         self.ctx[r] = ctx_len
@@ -507,6 +508,7 @@ class MXCache:
 
     def read(self, r, begin=0, end=None, first_step=0, n_steps=None, dtype=None):
         """Values of tokens begin..end-1 of request r: (k, v), each [n_steps][tokens][H][D]."""
+        r = range(self.batch)[r]
         end = self.ctx[r] if end is None else end
         n_steps = self.T - first_step if n_steps is None else n_steps
         if not 0 <= begin <= end <= self.ctx[r]:

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from sub_bit_vector_b200 import loopvq as L
-from test_mx_host import FAKE, UNSUP, _attn, _desc, _keep, _lay, _read, _write
+from test_mx_host import FAKE, UNSUP, _attn, _cache, _desc, _keep, _lay, _read, _write
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "sub_bit_vector_b200", "csrc")
 
@@ -127,3 +127,25 @@ def test_numbers_that_do_not_fit_refused(monkeypatch):
     for name in ("write", "read", "attn"):
         with pytest.raises(OverflowError):
             _prepare(name, loop_step=1 << 32)
+
+
+# ---------------------------------------------------------------- MXCache
+
+def test_requests_counted_from_the_end(monkeypatch):
+    """read(-1) names the last request as truncate(-1) does; it used to read no
+    request and return memory that nothing had written."""
+    c = _cache()
+    c.extend([5, 0, 70])
+    lays = []
+    monkeypatch.setattr(L, "loopvq_mx_read", lambda d, lay, *a: lays.append(lay))
+    for r in (2, -1):
+        c.read(r, 10, 64)
+        lay = lays.pop()
+        assert lay.total_new == lay.max_new == 54
+        assert [t.tolist() for t in lay._keep[:2]] == [[0, 0, 64], [0, 0, 0, 54]]
+    for call in (lambda r: c.read(r), lambda r: c.truncate(r, 0)):
+        for r in (3, -4):
+            with pytest.raises(IndexError):
+                call(r)
+    c.truncate(-1, 0)
+    assert c.ctx == [5, 0, 0]
