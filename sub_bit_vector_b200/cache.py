@@ -472,7 +472,8 @@ class MXCache:
     def attend(self, loop_step, q, tree_mask=None, softmax_scale=None, softcap=0.0, slopes=None):
         """Attention of the new tokens at loop_step: q [rows][Hq][D] -> (out
         [rows][Hq][D], lse [rows][Hq]).  tree_mask: int64 [rows], bit j of a
-        request's row i: its new token i sees its new token j (None: a chain)."""
+        request's row i: its new token i sees its new token j (None: a chain).
+        At most 64 new tokens per request: a longer prompt has a step of its own."""
         lay = self._step()
         self._rows(q, self.Hq, ())
         out = torch.empty((self.rows, self.Hq, self.D), dtype=self.out_dtype, device=self.device)
@@ -487,6 +488,7 @@ class MXCache:
     def keep(self, accepted) -> None:
         """accepted[r]: the new tokens of request r that stay, in the order
         that they take behind the prefix (None: all of them as they are).
+        Of more than 64 new tokens of a request all stay, or the first ones.
         Ends the step."""
         lay = self._step()
         if len(accepted) != self.batch:
@@ -495,11 +497,18 @@ class MXCache:
         for a, n in zip(lists, self.new):
             if len(a) > n or any(not 0 <= i < n for i in a):
                 raise ValueError("accepted tokens are indices of the request's new tokens")
-        if any(a != list(range(len(a))) for a in lists):   # else nothing moves
-            wide = max(len(a) for a in lists)
+        moves = [a != list(range(len(a))) for a in lists]
+        if any(moves):
+            sent = lists
+            if max(self.new) > 64:   # a prompt beside the trees: only the trees are sent
+                if max(n for n, m in zip(self.new, moves) if m) > 64:
+                    raise ValueError("of more than 64 new tokens only the first ones can be kept")
+                lay = self._layout(self.ctx, [n if m else 0 for n, m in zip(self.new, moves)])
+                sent = [a if m else [] for a, m in zip(lists, moves)]
+            wide = max(len(a) for a in sent)
             dev = dict(dtype=torch.int32, device=self.device)
-            L.loopvq_mx_keep(self.desc, lay, torch.tensor([a + [-1] * (wide - len(a)) for a in lists], **dev),
-                             torch.tensor([len(a) for a in lists], **dev), wide, self.poolK, self.poolV,
+            L.loopvq_mx_keep(self.desc, lay, torch.tensor([a + [-1] * (wide - len(a)) for a in sent], **dev),
+                             torch.tensor([len(a) for a in sent], **dev), wide, self.poolK, self.poolV,
                              self.fault_bits)
         ends = [c - n + len(a) for c, n, a in zip(self.ctx, self.new, lists)]
         for r, e in enumerate(ends):

@@ -8,15 +8,15 @@ import pytest
 import torch
 
 import oracle as O
-from sub_bit_vector_b200 import loopvq as L
-from test_gpu_mx import Setup, _filled, _i32, _queries, _run
+from sub_bit_vector_b200 import cache, loopvq as L
+from test_gpu_mx import Setup, _filled, _i32, _queries, _run, _values
 
 pytestmark = pytest.mark.gpu
 
 
-def _close(s, q, K, V, out, lse, *, cap=0.0, fine=False, scale=None, more=None, lost=None):
+def _close(s, q, K, V, out, lse, *, cap=0.0, fine=False, scale=None, more=None):
     """Chains of new tokens against the oracle.  ds = (32 * 2^-24 + 2^-22) B +
-    more(qq, k) per row; lost(p, v): what an output may lose besides."""
+    more(qq, k, B) per row."""
     scale = s.D ** -0.5 if scale is None else scale
     cap = float(np.float32(cap))
     G = s.Hq // s.H
@@ -32,10 +32,6 @@ def _close(s, q, K, V, out, lse, *, cap=0.0, fine=False, scale=None, more=None, 
             # two weights' scores are off by ds each: e^(2 ds) - 1, which is 2 ds where that is small
             w = np.expm1(np.minimum(2 * ds, 50.0)) + 2.0 ** -22 + (2.0 ** -21 if fine else 2.0 ** -11) + 2.0 ** -17
             tol = a * w[:, None] + c * 2.0 ** -32 * big + np.abs(o) * (2.0 ** -24 if s.out == "f32" else 2.0 ** -8) + 1e-37
-            if lost is not None:
-                x = np.where(sees, scale * (qq @ k.T), -np.inf)
-                p = np.exp(x - x.max(-1, keepdims=True))
-                tol = tol + lost(p / p.sum(-1, keepdims=True), v)
             err = np.abs(out[rows, hq] - o)
             assert (err <= tol).all(), (r, hq, float(np.max(err / tol)))
             assert (np.abs(lse[rows, hq] - l) <= ds + 2.0 ** -18 + 2.0 ** -22 * np.abs(l)).all(), (r, hq)
@@ -139,3 +135,28 @@ def test_kernels_that_follow_closely_see_the_last_ones_bytes(fmt, new):
     for a, b in zip(go(torch.cuda.synchronize), go(lambda: None)):
         assert torch.equal(a, b)
     assert s.faults() == 0
+
+
+def test_prompts_beside_trees_are_kept():
+    """A step with a prompt of more than 64 tokens, a tree and a single token: the
+    accepted nodes move, the rest stays."""
+    rng = np.random.default_rng(50)
+    c = cache.MXCache(n_loop=2, n_heads_kv=2, head_dim=64, batch=3, max_ctx_len=200, page_tokens=32, format="e2m1",
+                      out_dtype=torch.float32)
+    hist = [[np.zeros((2, 0, 2, 64))] * 2 for _ in range(3)]
+    for n_new, accept in (([40, 33, 0], None), ([100, 9, 1], [None, [0, 3, 8, 5], None]), ([1, 70, 6], [[], range(65), [5, 1]])):
+        c.extend(n_new)
+        X = [_values(rng, (2, c.rows, 2, 64), kind) for kind in "kv"]
+        c.write(*(torch.from_numpy(x).cuda() for x in X))
+        off = np.concatenate([[0], np.cumsum(n_new)])
+        if accept is not None:
+            c.keep(accept)
+        for r, n in enumerate(n_new):
+            a = list(range(n)) if accept is None or accept[r] is None else list(accept[r])
+            for i, x in enumerate(X):
+                back = O.mx_values(*O.mx_quantise(x[:, off[r]:off[r + 1]][:, a], "e2m1"), "e2m1")
+                hist[r][i] = np.concatenate([hist[r][i], back], 1)
+    for r in range(3):
+        for got, want in zip(c.read(r), hist[r]):
+            assert np.array_equal(got.double().cpu().numpy(), want)
+    assert c.device_faults() == 0

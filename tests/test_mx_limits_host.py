@@ -149,3 +149,24 @@ def test_requests_counted_from_the_end(monkeypatch):
                 call(r)
     c.truncate(-1, 0)
     assert c.ctx == [5, 0, 0]
+
+
+def test_a_prompt_beside_a_tree_is_kept(monkeypatch):
+    """The kernel takes up to 64 new tokens of a request; a prompt that stays as it
+    is, or loses its end, is not sent to it."""
+    sent = []
+    monkeypatch.setattr(L, "loopvq_mx_keep", lambda d, lay, keep, n, mx, *a: sent.append(
+        (keep.tolist(), n.tolist(), mx, lay.max_new, [t.tolist() for t in lay._keep[:2]])))
+    c = _cache()
+    c.extend([0, 30, 0])
+    c.extend([100, 5, 1])
+    with pytest.raises(ValueError, match="64"):
+        c.keep([[0, 2], [0], [0]])
+    assert c.ctx == [100, 35, 1] and not sent
+    c.keep([None, [0, 2], None])
+    assert sent == [([[-1, -1], [0, 2], [-1, -1]], [0, 2, 0], 2, 5, [[100, 35, 1], [0, 0, 5, 5]])]
+    assert c.ctx == [100, 32, 1]
+    c.extend([70, 5, 1])
+    c.keep([list(range(66)), [4], []])
+    assert sent[1:] == [([[-1], [4], [-1]], [0, 1, 0], 1, 5, [[170, 37, 2], [0, 0, 5, 5]])]
+    assert c.ctx == [166, 33, 1]
