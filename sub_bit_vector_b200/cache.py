@@ -367,9 +367,11 @@ class MXCache:
     ``keep`` moves the accepted tokens behind the prefix and drops the rest;
     ``truncate`` drops tokens at the end, ``read`` gives a range's values back.
     Every request's lengths are host state; device arrays are made anew by each
-    ``extend``, so calls that are still running on the GPU keep theirs.  All
-    calls go to torch's current stream; a caller that changes streams orders
-    them as for any tensor.
+    ``extend``, so calls that are still running on the GPU, on any stream, keep
+    theirs.  All calls go to torch's current stream; a caller that changes streams
+    orders them as for any tensor.  A CUDA graph captured from these calls has the
+    lengths and pages of its step, at every replay (``loopvq.prepare_mx_*`` with
+    the caller's own arrays serve graphs for many steps).
     """
 
     def __init__(self, *, n_loop, n_heads_kv, head_dim, batch, max_ctx_len, format="e4m3", page_tokens=256,
@@ -400,6 +402,7 @@ class MXCache:
         self.new = [0] * batch
         self.rows = 0
         self.layout = None
+        self.captured = []       # layouts that CUDA graphs read
 
     def _layout(self, ctx, new):
         off = [0]
@@ -428,6 +431,8 @@ class MXCache:
             self.pages[r] += [self.free.pop() for _ in range(n)]
         self.ctx, self.new, self.rows = grown, n_new, sum(n_new)
         self.layout = self._layout(self.ctx, self.new)
+        if self.device.type == "cuda":
+            self.made_on = torch.cuda.current_stream(self.device).cuda_stream
 
     def truncate(self, r, ctx_len) -> None:
         """Request r's context ends at ctx_len; its pages behind that are free
@@ -447,6 +452,16 @@ class MXCache:
     def _step(self):
         if self.layout is None:
             raise RuntimeError("extend() begins a step")
+        if self.device.type == "cuda":
+            # the arrays were made on another stream, maybe: their memory is not
+            # for new ones before this stream's calls are done; a graph's stays
+            stream = torch.cuda.current_stream(self.device)
+            if torch.cuda.is_current_stream_capturing():
+                if not any(lay is self.layout for lay in self.captured):
+                    self.captured.append(self.layout)
+            elif stream.cuda_stream != self.made_on:
+                for a in self.layout._keep:
+                    a.record_stream(stream)
         return self.layout
 
     # -------------------------------------------------------------- the step

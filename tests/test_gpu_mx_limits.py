@@ -160,3 +160,47 @@ def test_prompts_beside_trees_are_kept():
         for got, want in zip(c.read(r), hist[r]):
             assert np.array_equal(got.double().cpu().numpy(), want)
     assert c.device_faults() == 0
+
+
+def test_steps_on_another_stream_and_in_a_graph():
+    """A step's calls wait on a stream of their own while the host begins the next
+    steps, which make arrays of the same sizes; a graph of a step is replayed
+    after them."""
+    def steps(stream, wait):
+        rng = np.random.default_rng(60)
+        c = cache.MXCache(n_loop=1, n_heads_kv=2, n_heads_q=4, head_dim=64, batch=3, max_ctx_len=320, page_tokens=32)
+        res, graphs = [], []
+        torch.cuda.synchronize()
+        for i in range(6):
+            new = [int(x) for x in rng.integers(1, 9, 3)] if i else [100, 40, 64]
+            c.extend(new)
+            k, v = (torch.from_numpy(_values(rng, (c.rows, 2, 64), kind)).cuda().to(torch.bfloat16) for kind in "kv")
+            q = torch.from_numpy(rng.standard_normal((c.rows, 4, 64)).astype(np.float32)).cuda().to(torch.bfloat16)
+            torch.cuda.current_stream().synchronize()
+            with torch.cuda.stream(stream):
+                if wait:
+                    torch.cuda._sleep(20_000_000)       # about 10 ms: the calls below have not begun when extend returns
+                c.write(k, v, 0)
+                if max(new) <= 64:
+                    res.append(c.attend(0, q))
+            if i == 3:
+                torch.cuda.synchronize()
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g):
+                    res.append(c.attend(0, q))
+                graphs.append((g, q))
+            for x in (k, v, q):
+                x.record_stream(stream)
+        torch.cuda.synchronize()
+        for x in res[3]:                               # the graph's outputs: of its step, whatever came after
+            x.zero_()
+        for g, _ in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert c.device_faults() == 0
+        return [x.clone() for pair in res for x in pair]
+
+    plain = steps(torch.cuda.current_stream(), False)
+    for a, b in zip(plain, steps(torch.cuda.Stream(), True)):
+        assert torch.equal(a, b)
+    assert torch.equal(plain[6], plain[4]) and torch.equal(plain[7], plain[5])

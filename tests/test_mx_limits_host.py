@@ -170,3 +170,35 @@ def test_a_prompt_beside_a_tree_is_kept(monkeypatch):
     c.keep([list(range(66)), [4], []])
     assert sent[1:] == [([[-1], [4], [-1]], [0, 1, 0], 1, 5, [[170, 37, 2], [0, 0, 5, 5]])]
     assert c.ctx == [166, 33, 1]
+
+
+def test_a_steps_arrays_outlive_calls_on_other_streams_and_graphs(monkeypatch):
+    """The arrays that extend makes go back to the allocator with the next step.
+    Calls on another stream, which may still read them then, are made known to it;
+    a graph, which may read them at any time, keeps them."""
+    class Stream:
+        def __init__(self, number):
+            self.cuda_stream = number
+
+    class Array:
+        def __init__(self):
+            self.on = []
+
+        def record_stream(self, stream):
+            self.on.append(stream.cuda_stream)
+
+    now = {"stream": Stream(1), "capturing": False}
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: now["stream"])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now["capturing"])
+    c = _cache()
+    c.extend([3, 0, 0])
+    c.device, c.made_on = torch.device("cuda"), 1
+    c.layout._keep = [Array() for _ in range(3)]
+    assert c._step() is c.layout and all(a.on == [] for a in c.layout._keep)
+    now["stream"] = Stream(2)
+    c._step()
+    assert all(a.on == [2] for a in c.layout._keep) and c.captured == []
+    now["capturing"] = True
+    c._step()
+    c._step()
+    assert c.captured == [c.layout] and all(a.on == [2] for a in c.layout._keep)
