@@ -204,3 +204,129 @@ def test_steps_on_another_stream_and_in_a_graph():
     for a, b in zip(plain, steps(torch.cuda.Stream(), True)):
         assert torch.equal(a, b)
     assert torch.equal(plain[6], plain[4]) and torch.equal(plain[7], plain[5])
+
+
+@pytest.mark.parametrize("apart", [12, 20, 30])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_key_blocks_far_apart(D, types, apart):
+    """The first block of channels of every key 2^apart times as large as the
+    others, met by queries that are as much smaller there, or zero.
+
+    q is taken to half of 2^-38 of its row's largest element (fp32 too, whose
+    second term ends there): 2^-39 max|q| |k_d| per channel.  On the tensor cores
+    a key's element is taken to half of 2^-24 of 2^E, exactly if its block is
+    less than 2^15 below E's; 2^E <= 2 max|k| / 448: 2^-24 max|k| / 448 |q_d|."""
+    scale = D ** -0.5
+    for n, G in ROWS:
+        s = Setup([200 + n], [n], D=D, fmt="e4m3", H=1, Hq=G, seed=apart + n, page=64)
+        K = [_values(s.rng, (1, c, 1, D), "k") for c in s.ctx]
+        V = [_values(s.rng, (1, c, 1, D), "v") for c in s.ctx]
+        K[0][..., :32] *= 2.0 ** apart
+        s.write_all(K, V)
+        back = [[O.mx_values(*O.mx_quantise(x[0], "e4m3"), "e4m3") for x in X] for X in (K, V)]
+        for factor in (0.0, 2.0 ** -apart):
+            q = _queries(s, types[0])
+            q[..., :32] *= factor
+            o, l = _run(s, q, None, q_t=types[0], out_t=types[1])
+            on_tensor_cores = types[0] == "bf16" and n * G > 64
+
+            def more(qq, k, B):
+                d = scale * 2.0 ** -39 * np.abs(qq).max(-1) * np.abs(k).sum(-1).max()
+                if on_tensor_cores and apart > 12:
+                    d = d + scale * 2.0 ** -24 / 448 * np.abs(k).max() * np.abs(qq[:, 32:]).sum(-1)
+                return d
+            _close(s, q, *back, o, l, fine="f32" in types, more=more)
+        assert s.faults() == 0
+
+
+# ------------------------------------------------- lengths out of range
+
+BAD_LENGTHS = [([40, 251, 100], None), ([40, -1, 100], None), ([40, 2, 100], None), ([40, 50, 100], [0, 2, 1, 0]),
+               ([40, 50, 100], [0, 2, 30, 9])]
+
+
+def _batch():
+    s = Setup([40, 50, 100], [2, 3, 4], D=64, H=2, page=32, seed=12)
+    K, V = _filled(s)
+    return s, K, V
+
+
+def _valid(s, off):
+    """Requests that the bad lengths leave: all but the second, and if the
+    offsets are bad, the third too (its rows begin at a wrong place)."""
+    return (0, 2) if off is None else (0,)
+
+
+@pytest.mark.parametrize("ctx,off", BAD_LENGTHS)
+@pytest.mark.parametrize("many", [False, True])
+def test_writes_of_bad_lengths_touch_nothing(ctx, off, many):
+    """Both kernels of the write (few tokens, whole tiles): the pools' bytes are
+    the oracle's for the requests that are in range, and the old ones elsewhere."""
+    s, _, _ = _batch()
+    want = [p.cpu().numpy().copy() for p in (s.poolK, s.poolV)]
+    X = [_values(s.rng, (s.rows, s.H, s.D), kind) for kind in "kv"]
+    k, v = (torch.from_numpy(x).cuda() for x in X)
+    lay = s.layout(ctx, s.off if off is None else off, max_ctx_len=100, max_new=20 if many else 4, total_new=9)
+    L.loopvq_mx_write(s.desc, lay, 0, 1, k, v, 0, s.H * s.D, s.D, s.poolK, s.poolV, s.fault)
+    assert s.faults() == L.LOOPVQ_FAULT_CTX_RANGE
+    ok = _valid(s, off)
+    for kind, x, w, pool in (("k", X[0], want[0], s.poolK), ("v", X[1], want[1], s.poolV)):
+        code, scale = O.mx_quantise(x, s.fmt)
+        for r in ok:
+            for i in range(s.new[r]):
+                for h in range(s.H):
+                    O.mx_store(w, 0, h, s.pos(r, s.ctx[r] - s.new[r] + i), code[s.off[r] + i, h], scale[s.off[r] + i, h],
+                               kind, s.fmt)
+        np.testing.assert_array_equal(pool.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("ctx,off", BAD_LENGTHS)
+def test_keeps_of_bad_lengths_touch_nothing(ctx, off):
+    """Index 1 to place 0 moves bytes: of the requests in range, and no others."""
+    s, _, _ = _batch()
+    before = [p.cpu().numpy().copy() for p in (s.poolK, s.poolV)]
+    lay = s.layout(ctx, s.off if off is None else off, max_ctx_len=100, max_new=4, total_new=9)
+    L.loopvq_mx_keep(s.desc, lay, _i32([[1], [1], [1]]), _i32([1, 1, 1]), 1, s.poolK, s.poolV, s.fault)
+    assert s.faults() == L.LOOPVQ_FAULT_CTX_RANGE
+    for kind, w, pool in (("k", before[0], s.poolK), ("v", before[1], s.poolV)):
+        old = w.copy()
+        for r in _valid(s, off):
+            P = s.ctx[r] - s.new[r]
+            src, dst = s.pos(r, P + 1), s.pos(r, P)
+            for h in range(s.H):
+                code = np.array([old[0, h, src // 32][O.mx_place(src % 32, d, kind, s.D, s.fmt)[0]] for d in range(s.D)])
+                scale = np.array([old[0, h, src // 32][O.mx_scale_place(src % 32, b, s.D, s.fmt)] for b in range(s.D // 32)])
+                O.mx_store(w, 0, h, dst, code, scale, kind, s.fmt)
+        assert not np.array_equal(w, old)
+        np.testing.assert_array_equal(pool.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("ctx,off", BAD_LENGTHS)
+@pytest.mark.parametrize("many", [False, True])
+def test_reads_and_attention_of_bad_lengths_leave_rows(ctx, off, many):
+    """Rows of the requests in range are right, all others stay as they were; few
+    tokens and whole tiles, the warps' attention and the tensor cores'."""
+    s, K, V = _batch()
+    Hq = 64 if many else 2
+    s.desc, s.Hq = L.make_mx_desc(1, s.H, s.D, L.LOOPVQ_MX_E4M3, n_heads_q=Hq), Hq
+    q = _queries(s, "bf16")
+    lay = s.layout(ctx, s.off if off is None else off, max_ctx_len=100, max_new=20 if many else 4, total_new=9)
+    o, l = _run(s, q, None, lay=lay)
+    assert s.faults() == L.LOOPVQ_FAULT_CTX_RANGE
+    s.fault.zero_()
+    ko, vo = (torch.full((1, s.rows, s.H, s.D), 7.0, device="cuda") for _ in "kv")
+    L.loopvq_mx_read(s.desc, lay, 0, 1, s.poolK, s.poolV, ko, vo, 0, s.H * s.D, s.D, s.fault)
+    assert s.faults() == L.LOOPVQ_FAULT_CTX_RANGE
+    ko, vo = ko.double().cpu().numpy()[0], vo.double().cpu().numpy()[0]
+    rows = np.zeros(s.rows, dtype=bool)
+    new = [0] * 3
+    for r in _valid(s, off):
+        rows[s.off[r]:s.off[r + 1]] = True
+        new[r] = s.new[r]
+        P = s.ctx[r] - s.new[r]
+        assert np.array_equal(ko[s.off[r]:s.off[r + 1]], K[r][P:]) and np.array_equal(vo[s.off[r]:s.off[r + 1]], V[r][P:])
+    for x in (o, l, ko, vo):
+        assert (x[~rows] == 7).all()
+    s.new = new
+    _close(s, q, K, V, o, l)
