@@ -404,12 +404,12 @@ class MXCache:
         self.layout = None
         self.captured = []       # layouts that CUDA graphs read
 
-    def _layout(self, ctx, new):
+    def _layout(self, ctx, new, pages=None):
         off = [0]
         for n in new:
             off.append(off[-1] + n)
         dev = dict(dtype=torch.int32, device=self.device)
-        table = [p + [-1] * (self.max_pages - len(p)) for p in self.pages]
+        table = [p + [-1] * (self.max_pages - len(p)) for p in pages or self.pages]
         return L.make_mx_layout(self.batch, self.page_tokens, self.max_pages, self.pool_tokens, self.max_ctx_len,
                                 max(new), off[-1], torch.tensor(ctx, **dev), torch.tensor(off, **dev),
                                 torch.tensor(table, **dev))
@@ -427,10 +427,11 @@ class MXCache:
         need = [-(-c // self.page_tokens) - len(p) for c, p in zip(grown, self.pages)]
         if sum(need) > len(self.free):
             raise RuntimeError("cache out of pages")
-        for r, n in enumerate(need):
-            self.pages[r] += [self.free.pop() for _ in range(n)]
-        self.ctx, self.new, self.rows = grown, n_new, sum(n_new)
-        self.layout = self._layout(self.ctx, self.new)
+        taken = reversed(self.free)
+        pages = [p + [next(taken) for _ in range(n)] for p, n in zip(self.pages, need)]
+        self.layout = self._layout(grown, n_new, pages)    # if that fails, nothing has changed
+        del self.free[len(self.free) - sum(need):]
+        self.pages, self.ctx, self.new, self.rows = pages, grown, n_new, sum(n_new)
         if self.device.type == "cuda":
             self.made_on = torch.cuda.current_stream(self.device).cuda_stream
 

@@ -202,3 +202,23 @@ def test_a_steps_arrays_outlive_calls_on_other_streams_and_graphs(monkeypatch):
     c._step()
     c._step()
     assert c.captured == [c.layout] and all(a.on == [2] for a in c.layout._keep)
+
+
+def test_an_extend_that_fails_changes_nothing(monkeypatch):
+    """No memory for the arrays of a step, or a stream that is being captured: the
+    cache is as it was, and the same extend may be tried again."""
+    c = _cache()
+    c.extend([40, 3, 0])
+    before = [list(c.ctx), list(c.new), c.rows, [list(p) for p in c.pages], list(c.free), c.layout]
+
+    def fail(*a):
+        raise RuntimeError("out of memory")
+
+    with monkeypatch.context() as m:
+        m.setattr(L, "make_mx_layout", fail)
+        with pytest.raises(RuntimeError, match="out of memory"):
+            c.extend([30, 1, 65])
+    assert before == [c.ctx, c.new, c.rows, c.pages, c.free, c.layout]
+    c.extend([30, 1, 65])
+    assert c.ctx == [70, 4, 65] and [len(p) for p in c.pages] == [3, 1, 3] and len(c.free) == 5
+    assert sorted(sum(c.pages, []) + c.free) == list(range(12))
