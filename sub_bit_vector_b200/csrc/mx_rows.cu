@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
       MxReq rq = {};
       mx_request(p.L, cc.r, &rq, nullptr);
       const int chunks = cc.units / p.H, h = cc.u / chunks, rho0 = (cc.u - h * chunks) * CHUNK;
-      const int rows = min(CHUNK, rq.n * p.G - rho0);
+      const int rows = max(0, min(CHUNK, rq.n * p.G - rho0));   // 0 if lengths change meanwhile
       const int first_tile = cc.t, n_tiles = min(cc.tiles - cc.t, count - done);
       const uint64_t all_new = rq.n >= 64 ? ~0ull : (1ull << rq.n) - 1;
       // the row: scaled by a power of two to a largest magnitude in [2^14, 2^15),
