@@ -330,3 +330,105 @@ def test_reads_and_attention_of_bad_lengths_leave_rows(ctx, off, many):
         assert (x[~rows] == 7).all()
     s.new = new
     _close(s, q, K, V, o, l)
+
+
+# ------------------------------------------------- calls that stand elsewhere
+
+def test_captured_after_other_nodes():
+    """A graph in which these kernels follow nothing, a copy, a fill, a kernel of
+    torch and a join of two streams: replays give what eager calls give."""
+    s = Setup([200, 90], [6, 3], seed=70, D=64, Hq=4)
+    _filled(s)
+    src = torch.from_numpy(s.rng.standard_normal((2, s.rows, 2, 64)).astype(np.float32)).cuda().to(torch.bfloat16)
+    x, q = torch.zeros_like(src), torch.zeros((2, s.rows, 4, 64), dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros((3, s.rows, 4, 64), dtype=torch.bfloat16, device="cuda")
+    back = torch.zeros((2, 1, s.rows, 2, 64), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros((2, L.loopvq_mx_attn_workspace_bytes(s.desc, s.lay)), dtype=torch.uint8, device="cuda")
+
+    def write():
+        L.loopvq_mx_write(s.desc, s.lay, 0, 1, x[0], x[1], 0, 128, 64, s.poolK, s.poolV, s.fault)
+
+    def read():
+        L.loopvq_mx_read(s.desc, s.lay, 0, 1, s.poolK, s.poolV, back[0], back[1], 0, 128, 64, s.fault)
+
+    def attn(i, w=0):
+        L.loopvq_mx_attn(s.desc, s.lay, s.poolK, s.poolV, q[i // 2], 256, 64, None, 0, 0.125, 0.0, None, out[i], None, ws[w],
+                         s.fault)
+
+    side = torch.cuda.Stream()
+
+    def go():
+        main = torch.cuda.current_stream()
+        attn(0)                              # follows nothing
+        x.copy_(src)                         # a copy
+        write()
+        side.wait_stream(main)
+        q[0].copy_(src[0].repeat(1, 2, 1))   # kernels of torch, beside the read
+        with torch.cuda.stream(side):
+            read()
+        main.wait_stream(side)
+        attn(1)                              # a join
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            attn(0, 1)                       # beside the next call, with a workspace of its own
+        q[1].fill_(0.25)                     # a fill
+        attn(2)
+        main.wait_stream(side)
+        read()
+
+    pools = s.poolK.clone(), s.poolV.clone()
+
+    def again(run):
+        s.poolK.copy_(pools[0])
+        s.poolV.copy_(pools[1])
+        for t in (x, q, out, back):
+            t.zero_()
+        torch.cuda.synchronize()
+        run()
+        torch.cuda.synchronize()
+        return [t.clone() for t in (out, back, s.poolK, s.poolV)]
+
+    def one_at_a_time():
+        for step in (lambda: attn(0), lambda: x.copy_(src), write, read, lambda: q[0].copy_(src[0].repeat(1, 2, 1)),
+                     lambda: attn(1), lambda: attn(0, 1), lambda: q[1].fill_(0.25), lambda: attn(2)):
+            step()
+            torch.cuda.synchronize()
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        go()
+    want = again(one_at_a_time)
+    for _ in range(3):
+        for a, b in zip(want, again(g.replay)):
+            assert torch.equal(a, b)
+    assert s.faults() == 0
+
+
+@pytest.mark.parametrize("Hq", [1, 4])
+def test_requests_that_share_the_pages_of_a_prefix(Hq):
+    """40 requests (more than a warp has lanes) whose tables begin with the same
+    pages, 17 to 30 tokens each behind them; a query of NaN and one of
+    infinities among the rows; the warps' kernel and the tensor cores."""
+    n, D, page = 17, 64, 32
+    rng = np.random.default_rng(80)
+    new = [n + int(x) for x in rng.integers(0, 14, 40)]
+    s = Setup([96 + x for x in new], new, D=D, fmt="e4m3", H=1, Hq=Hq, seed=81, page=page)
+    s.table[:, :3] = s.table[0, :3]
+    s.lay = s.layout(s.ctx, s.off)
+    pre = [_values(rng, (1, 96, 1, D), kind) for kind in "kv"]
+    own = [[_values(rng, (1, x, 1, D), kind) for x in new] for kind in "kv"]
+    k, v = (torch.from_numpy(x).cuda() for x in pre)
+    L.loopvq_mx_write(s.desc, s.layout([96] + [0] * 39, [0] + [96] * 40), 0, 1, k, v, 0, D, D, s.poolK, s.poolV, s.fault)
+    k, v = (torch.from_numpy(np.concatenate(x, 1)).cuda() for x in own)
+    L.loopvq_mx_write(s.desc, s.lay, 0, 1, k, v, 0, D, D, s.poolK, s.poolV, s.fault)
+    back = [[O.mx_values(*O.mx_quantise(np.concatenate([p, x], 1)[0], "e4m3"), "e4m3") for x in o] for p, o in zip(pre, own)]
+    q = _queries(s, "bf16")
+    o, l = _run(s, q, None)
+    _close(s, q, *back, o, l)
+    bad = q.copy()
+    bad[3, 0, 5], bad[100, Hq - 1, 9] = np.nan, np.inf
+    o2, _ = _run(s, bad, None)
+    same = np.ones((s.rows, Hq), dtype=bool)
+    same[3, 0] = same[100, Hq - 1] = False
+    assert np.array_equal(o2[same], o[same]) and np.isnan(o2[~same]).all()
+    assert s.faults() == 0
