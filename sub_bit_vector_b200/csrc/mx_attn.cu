@@ -80,7 +80,8 @@ struct MxRows {
   static constexpr int kPerGroup = NARROW ? 8 / (D / kMxBlock) / NARROW : 8;
 };
 
-template <int D, int FMT, int NARROW, int TERMS, int NT>
+// TERMS: fp16 terms of queries and weights; EXACT: the cap's tanh (kFastCap).
+template <int D, int FMT, int NARROW, int TERMS, int NT, bool EXACT>
 __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32, 1) mx_attn_kernel(const MxAttnParams p) {
   using Tile = MxTile<D, FMT>;
   using Ring = MxRing<D, FMT, NARROW, NT>;
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       const int ex = max((int)(__float_as_uint(mx) >> 23), 1) - 127;
       const int k2 = min(14 - ex, 120);
-      const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
-      f[i] = p.scale * down * (p.softcap > 0.f ? 1.f : kLog2e);
+      const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(129 - k2) << 23);
+      f[i] = p.scale * down;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -390,11 +391,11 @@ __global__ void __launch_bounds__((MxRing<D, FMT, NARROW, NT>::kWarps + 1) * 32,
             }
           }
           if (p.softcap > 0.f) {
-            const bool fast = TERMS == 1 && p.softcap <= kFastCap;
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-              for (int t = 0; t < 4; ++t) x[i][t] = fast ? capped_fast(x[i][t], p.softcap, p.inv_cap) : capped(x[i][t], p.softcap, p.inv_cap);
+              for (int t = 0; t < 4; ++t)
+                x[i][t] = EXACT ? capped(x[i][t], p.softcap, p.inv_cap) : capped_fast(x[i][t], p.softcap, p.inv_cap2);
           }
           if (p.slopes || edge) {
 #pragma unroll
@@ -860,7 +861,8 @@ loopvq_status launch_merge(const MxAttnParams& p, int64_t rows, cudaStream_t s) 
 template <int D, int FMT, int NARROW, int TERMS, int NT>
 loopvq_status launch_attn(const MxAttnParams& p, int grid, int64_t rows, cudaStream_t s) {
   constexpr int smem = MxRing<D, FMT, NARROW, NT>::kBytes, W = MxRing<D, FMT, NARROW, NT>::kWarps, CHUNK = MxRows<D, NARROW>::kPerGroup * NT;
-  auto kfn = mx_attn_kernel<D, FMT, NARROW, TERMS, NT>;
+  auto kfn = TERMS == 2 || p.softcap > kFastCap ? mx_attn_kernel<D, FMT, NARROW, TERMS, NT, true>
+                                                : mx_attn_kernel<D, FMT, NARROW, TERMS, NT, TERMS == 2>;
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return LOOPVQ_ERR_CUDA;
   if (mx_launch(kfn, dim3(grid), (W + 1) * 32, smem, s, p) != cudaSuccess) return LOOPVQ_ERR_CUDA;
   return launch_merge<D, CHUNK>(p, rows, s);
@@ -954,9 +956,10 @@ extern "C" loopvq_status loopvq_mx_attn(const loopvq_mx_desc* desc, const loopvq
   p.qn = q_stride_n;
   p.qh = q_stride_h;
   p.tree_mask = tree_mask;
-  p.scale = softmax_scale;
   p.softcap = softcap;
+  p.scale = softmax_scale * (softcap > 0.f ? 0.25f : 0.25f * kLog2e);
   p.inv_cap = softcap > 0.f ? std::fmin(1.f / softcap, 0x1p126f) : 0.f;   // of a smaller cap every score but 0 is at it
+  p.inv_cap2 = 2.f * kLog2e * p.inv_cap;
   p.slopes = slopes;
   p.out = out;
   p.out_bf16 = out_dtype == LOOPVQ_BF16;

@@ -16,7 +16,8 @@ struct MxAttnParams {
   int q_bf16, q_vec;
   int64_t qn, qh;
   const uint64_t* tree_mask;
-  float scale, softcap, inv_cap;   // inv_cap: 1 / softcap, at most 2^126
+  float scale;   // a quarter (no product overflows) of softmax_scale, times log2 e unless a cap wants natural units
+  float softcap, inv_cap, inv_cap2;   // inv_cap: 1 / softcap, at most 2^126; inv_cap2 = 2 log2(e) inv_cap
   const float* slopes;
   void* out;
   int out_bf16;
@@ -39,14 +40,14 @@ __device__ __forceinline__ float tanh_abs(float y2) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(y2)));
   return fmaf(-2.f, r, 1.f);
 }
-// Score s, capped, in log2 units; inv: 1 / cap.  tanh_abs misses s by 2^-22 of the
-// cap, however small s is: with a cap up to kFastCap by 2^-16, 1/32 of what the
-// rounding of a weight to fp16 loses.  Above, and with fp32 in or out, tanhf,
-// whose error is relative to s (s / cap in steps of 2^-149, s of 2^-21 at most).
+// Score s, capped, in log2 units.  tanh_abs misses s by 2^-22 of the cap, however
+// small s is: with a cap up to kFastCap by 2^-16, 1/32 of what the rounding of a
+// weight to fp16 loses.  Above, and with fp32 in or out, tanhf, whose error is
+// relative to s (s / cap in steps of 2^-149, s of 2^-21 at most).  64-node tree over
+// 32K: 138 us with tanh_abs, 162 with tanhf; chosen per score in one kernel instead of
+// in instances of their own (EXACT) 218, since both are computed then.
 constexpr float kFastCap = 64.f;
-__device__ __forceinline__ float capped_fast(float s, float cap, float inv) {
-  return cap * kLog2e * tanh_abs(s * (2.f * kLog2e * inv));
-}
+__device__ __forceinline__ float capped_fast(float s, float cap, float inv2) { return cap * kLog2e * tanh_abs(s * inv2); }
 __device__ __forceinline__ float capped(float s, float cap, float inv) { return cap * tanhf(s * inv) * kLog2e; }
 // 8 channels of a query row.
 template <typename T>

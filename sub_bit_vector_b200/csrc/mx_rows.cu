@@ -145,15 +145,7 @@ __device__ __forceinline__ float ratio(float e, float E) {
   return __int_as_float(max(__float_as_int(e) - __float_as_int(E) + 0x3f800000, 0));
 }
 
-// capped(), with s itself where tanh y is y to 2^-25.  Not for its result: with it the
-// kernel takes 114.5 us where it takes 117.3 without (64-node tree, 32K, no cap), 115.7
-// before there were large caps.
-__device__ __forceinline__ float capped_row(float s, float cap, float inv) {
-  const float y = s * inv;
-  return (fabsf(y) < 0x1p-12f ? s : cap * tanhf(y)) * kLog2e;
-}
-
-template <int D, int FMT>
+template <int D, int FMT, bool EXACT>
 __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnParams p) {
   using R = Rows<D, FMT>;
   using Tile = MxTile<D, FMT>;
@@ -474,8 +466,8 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         for (int k = 0; k < D / 2; ++k) mx = fmaxf(mx, fmaxf(fabsf(bf16_lo(q[k])), fabsf(bf16_hi(q[k]))));
         const int ex = max((int)(__float_as_uint(mx) >> 23), 1) - 127;
         const int k2 = min(14 - ex, 120);
-        const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(127 - k2) << 23);
-        f = p.scale * down * (p.softcap > 0.f ? 1.f : kLog2e);
+        const float up = __uint_as_float((uint32_t)(127 + k2) << 23), down = __uint_as_float((uint32_t)(129 - k2) << 23);
+        f = p.scale * down;
 #pragma unroll
         for (int k = 0; k < D / 32; ++k) {
           uint32_t z[16];
@@ -517,7 +509,7 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
         if (p.softcap > 0.f) {
 #pragma unroll
           for (int t = 0; t < 32; ++t)
-            x[t] = p.softcap <= kFastCap ? capped_fast(x[t], p.softcap, p.inv_cap) : capped_row(x[t], p.softcap, p.inv_cap);
+            x[t] = EXACT ? capped(x[t], p.softcap, p.inv_cap) : capped_fast(x[t], p.softcap, p.inv_cap2);
         }
         if (p.slopes) {
 #pragma unroll
@@ -691,10 +683,10 @@ __global__ void __launch_bounds__(kRowsThreads, 2) mx_rows_kernel(const MxAttnPa
 template <int D, int FMT>
 cudaError_t launch(const MxAttnParams& p, int grid, cudaStream_t s) {
   constexpr int smem = Rows<D, FMT>::kBytes;
-  const cudaError_t e =
-      cudaFuncSetAttribute(mx_rows_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kfn = p.softcap > kFastCap ? mx_rows_kernel<D, FMT, true> : mx_rows_kernel<D, FMT, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return mx_launch(mx_rows_kernel<D, FMT>, dim3(grid), kRowsThreads, smem, s, p);
+  return mx_launch(kfn, dim3(grid), kRowsThreads, smem, s, p);
 }
 
 }  // namespace
