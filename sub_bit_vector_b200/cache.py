@@ -467,7 +467,7 @@ class MXCache:
 
     # -------------------------------------------------------------- the step
     def _rows(self, x, heads, lead):
-        if tuple(x.shape) != (*lead, self.rows, heads, self.D) or x.stride(-1) != 1:
+        if tuple(x.shape) != (*lead, self.rows, heads, self.D) or (x.numel() and x.stride(-1) != 1):
             raise ValueError(f"expected {[*lead, self.rows, heads, self.D]} with consecutive channels, "
                              f"got {list(x.shape)}")
 

@@ -222,3 +222,18 @@ def test_an_extend_that_fails_changes_nothing(monkeypatch):
     c.extend([30, 1, 65])
     assert c.ctx == [70, 4, 65] and [len(p) for p in c.pages] == [3, 1, 3] and len(c.free) == 5
     assert sorted(sum(c.pages, []) + c.free) == list(range(12))
+
+
+def test_idle_steps_take_empty_rows_of_any_strides(monkeypatch):
+    """No request has a new token: rows without elements, whose strides mean
+    nothing, are no error."""
+    calls = []
+    monkeypatch.setattr(L, "loopvq_mx_write", lambda d, lay, *a: calls.append(lay.total_new))
+    c = _cache()
+    c.extend([0, 0, 0])
+    empty = torch.zeros(0).as_strided((0, 1, 64), (64, 64, 3))
+    c.write(empty, empty, 0)
+    assert calls == [0]
+    c.extend([1, 0, 0])
+    with pytest.raises(ValueError, match="consecutive channels"):
+        c.write(torch.zeros((1, 1, 128))[..., ::2], torch.zeros((1, 1, 64)), 0)
