@@ -608,7 +608,8 @@ typedef struct {
  * (CTX_RANGE) leaves that request out, its rows and tokens as they were; a
  * page id outside the pool (POOL_RANGE) leaves out that page's tokens; a
  * bounded wait that gave up sets TIMEOUT, and the call's output is undefined.
- * Pages written in one call must not be shared between its requests.
+ * Pages written in one call must not be shared between its requests, nor stand
+ * twice in a request's table.
  */
 typedef struct {
   int32_t batch;             /* 1 .. 65535 */
@@ -675,8 +676,9 @@ LOOPVQ_API size_t loopvq_mx_attn_workspace_bytes(const loopvq_mx_desc* desc, con
  *   q         : device, (row, hq, d) at row*q_stride_n + hq*q_stride_h + d in
  *               q_dtype.  Query head hq reads KV head hq / (Hq / H).
  *   slopes    : device fp32 [Hq], or NULL.
- *   out       : device [total_new][Hq][D] in out_dtype, 16-byte aligned; lse_out: device fp32
- *               [total_new][Hq] natural log-sum-exp, or NULL.
+ *   out       : device [total_new][Hq][D] in out_dtype, 16-byte aligned, not q's
+ *               memory; lse_out: device fp32 [total_new][Hq] natural
+ *               log-sum-exp, or NULL.
  *   workspace : device, 256-byte aligned; needs no initialisation, holds
  *               nothing between calls.  Calls that may overlap on the GPU
  *               (two streams, two graphs) need one each.

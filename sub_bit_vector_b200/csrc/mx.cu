@@ -13,8 +13,8 @@
 // CTA take neighbouring heads, whose rows are neighbours in x.  An 8K prompt of
 // 16 heads x 128 and 4 steps, bf16 to e2m1, is written in 67 us (339 MB: 5.1 TB/s;
 // the ALU pipe is at two thirds, 12 instructions per 32 elements, most of them
-// for the blocks' maxima and scales); a 16K context, e4m3 to bf16, is read in 128
-// us (814 MB: 6.4 TB/s, 97% of a copy).  For a few tokens see MxQuad.
+// for the blocks' maxima and scales); a 16K context, e4m3 to bf16, is read in 130
+// us (814 MB: 6.25 TB/s, 95% of a copy).  For a few tokens see MxQuad.
 #include "mx.cuh"
 
 namespace loopvq {

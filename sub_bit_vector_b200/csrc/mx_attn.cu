@@ -26,12 +26,19 @@
 // 2^8: halfway between fp16's top and where its 11 bits begin to run out, at
 // 2^-22 of the largest weight.
 //
-// Bounds (16 heads x 128, B200): 32 requests of 6-18K tokens, e4m3, trees of up
-// to 8: 235 us, 6.2 TB/s, 95% of a copy.  One row each, e2m1: 150 us, 5.35 TB/s: 410
-// instructions per tile of 32 tokens, tensor pipe 42%, issue slots 52%, the
-// slowest SM 10% behind the median.  One token over 32K, e4m3: 34 us against 21
-// of bytes: 3 us until the lengths, the page and the first tile have come one
-// after another, 4 us for the merge, and shares of only 10 tiles per warp.
+// With bf16 queries and outputs the weights are one fp16 term: their 11 bits are 3
+// more than the output keeps, and the error against 64 bits is that of the
+// output's rounding (0.00165 relative; 0.00164 with fp32 weights).  With fp32 in or
+// out there are two terms.
+//
+// Bounds (16 heads x 128; one call, inputs not in L2; B200s differ): 32 requests of
+// 6-18K tokens, e4m3, trees of up to 8: 250 to 275 us, 5.3 to 5.8 TB/s, 81 to 89% of
+// a copy.  One row each, e2m1: 156 to 168 us, 4.8 to 5.1 TB/s: 410 instructions per tile
+// of 32 tokens, tensor pipe 42%, issue slots 52%, the slowest SM 10% behind the
+// median.  One token over 32K, e4m3: 34 us against 21 of bytes: 3 us until the
+// lengths, the page and the first tile have come one after another, 4 us for the
+// merge, and shares of only 10 tiles per warp.  mx_attn_kernel<128, e4m3, 0, 1, 1> keeps
+// its 12 warps at the price of 120 bytes of spills.
 #include <cmath>
 
 #include "mx_attn.cuh"
@@ -72,9 +79,9 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
 //   NARROW 2: a column is a (half of the tile, query row, block): one such
 //             pass covers both halves.  The halves are summed at the end as
 //             two parts of a split context.
-// Measured on 32 requests of 6-18K tokens, one row each, e2m1, D = 128: kind 0
-// 249 us, kind 1 181 us, kind 2 161 us (149 since a warp of its own feeds the
-// rings).
+// Measured on 32 requests of 6-18K tokens, one row each, e2m1, D = 128, replayed in a
+// graph: kind 0 249 us, kind 1 181 us, kind 2 161 us (149 since a warp of its own
+// feeds the rings).
 template <int D, int NARROW>
 struct MxRows {
   static constexpr int kPerGroup = NARROW ? 8 / (D / kMxBlock) / NARROW : 8;

@@ -19,10 +19,13 @@
 // and scores are double-buffered, so that tile i's softmax, tile i + 1's scores
 // and the product P V of tile i - 1 run together.
 //
+// P is one fp16 term, as in mx_attn.cu and for its reason.
+//
 // A tree of 64 nodes, two query heads per KV head, over 32K tokens of 16 heads x
-// 128, e2m1: 113 us (the warps' kernel 253).  34 GFLOP would take 21 us; what
-// bounds it are the 3000 instructions of the softmax and the conversion per tile
-// at 0.47 issued per cycle and scheduler (16 warps per SM, 128 registers each).
+// 128, e2m1: 115 us (the warps' kernel 253).  34 GFLOP would take 21 us.  Issue slots
+// are 47% and the tensor pipe 14% busy: the 16 warps of an SM (128 registers each,
+// 264 bytes of a row's query spilled at D = 128, 44 at 64) mostly wait for one another, at
+// a block barrier and five mbarriers per 32 tokens.
 //
 // Operands in shared memory are K-major without swizzle: core matrices of 8
 // rows x 16 bytes, at (row / 8) * SBO + (k / 8) * LBO.  LBO and SBO are padded so
