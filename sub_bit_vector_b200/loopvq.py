@@ -419,6 +419,11 @@ def _mx_rows(desc, layout, first_step, n_steps, a, b, stride_t, stride_n, stride
         _want_strided("v", b, last)
 
 
+def _copied(struct):
+    """A pointer to ``struct`` as it was checked, whatever becomes of it."""
+    return ctypes.byref(type(struct).from_buffer_copy(struct))
+
+
 def _prepared(name, args, keep, stream):
     """A zero-argument call of entry point ``name``; without a stream, on
     torch's current one at the time of each call."""
@@ -457,7 +462,7 @@ def prepare_mx_write(desc, layout, first_step, n_steps, k, v, stride_t, stride_n
     _mx_buffers(desc, layout, poolK, poolV, fault_bits)
     _mx_rows(desc, layout, first_step, n_steps, k, v, stride_t, stride_n, stride_h)
     return _prepared("loopvq_mx_write", (
-        ctypes.byref(desc), ctypes.byref(layout), first_step, n_steps, _ptr(k), _ptr(v), _dtype_code(k), stride_t,
+        _copied(desc), _copied(layout), first_step, n_steps, _ptr(k), _ptr(v), _dtype_code(k), stride_t,
         stride_n, stride_h, _ptr(poolK), _ptr(poolV), _ptr(fault_bits)),
         (desc, layout, k, v, poolK, poolV, fault_bits), stream)
 
@@ -477,7 +482,7 @@ def prepare_mx_read(desc, layout, first_step, n_steps, poolK, poolV, k_out, v_ou
     _mx_buffers(desc, layout, poolK, poolV, fault_bits)
     _mx_rows(desc, layout, first_step, n_steps, k_out, v_out, stride_t, stride_n, stride_h)
     return _prepared("loopvq_mx_read", (
-        ctypes.byref(desc), ctypes.byref(layout), first_step, n_steps, _ptr(poolK), _ptr(poolV), _ptr(k_out),
+        _copied(desc), _copied(layout), first_step, n_steps, _ptr(poolK), _ptr(poolV), _ptr(k_out),
         _ptr(v_out), _dtype_code(k_out), stride_t, stride_n, stride_h, _ptr(fault_bits)),
         (desc, layout, k_out, v_out, poolK, poolV, fault_bits), stream)
 
@@ -509,7 +514,7 @@ def prepare_mx_attn(desc, layout, poolK, poolV, q, q_stride_n, q_stride_h, tree_
     if rows and q_stride_n >= 0 and q_stride_h >= 0:
         _want_strided("q", q, (rows - 1) * q_stride_n + (Hq - 1) * q_stride_h + D - 1)
     return _prepared("loopvq_mx_attn", (
-        ctypes.byref(desc), ctypes.byref(layout), _ptr(poolK), _ptr(poolV), _ptr(q), _dtype_code(q), q_stride_n,
+        _copied(desc), _copied(layout), _ptr(poolK), _ptr(poolV), _ptr(q), _dtype_code(q), q_stride_n,
         q_stride_h, _ptr(tree_mask), loop_step, softmax_scale, softcap, _ptr(slopes), _ptr(out), _dtype_code(out),
         _ptr(lse_out), _ptr(workspace), _nbytes(workspace), _ptr(fault_bits)),
         (desc, layout, q, tree_mask, slopes, out, lse_out, workspace, poolK, poolV, fault_bits), stream)
@@ -530,7 +535,7 @@ def prepare_mx_keep(desc, layout, keep, n_keep, max_keep, poolK, poolV, fault_bi
     _want("keep", keep, ("int32",), layout.batch * max(0, max_keep))
     _want("n_keep", n_keep, ("int32",), layout.batch)
     return _prepared("loopvq_mx_keep", (
-        ctypes.byref(desc), ctypes.byref(layout), _ptr(keep), _ptr(n_keep), max_keep, _ptr(poolK), _ptr(poolV),
+        _copied(desc), _copied(layout), _ptr(keep), _ptr(n_keep), max_keep, _ptr(poolK), _ptr(poolV),
         _ptr(fault_bits)), (desc, layout, keep, n_keep, poolK, poolV, fault_bits), stream)
 
 

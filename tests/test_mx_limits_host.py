@@ -88,6 +88,18 @@ def test_layouts_made_by_hand_are_taken(name, monkeypatch):
     assert _prepare(name, lay=lay) == "prepared"
 
 
+@pytest.mark.parametrize("name", CALLS)
+def test_prepared_calls_keep_what_was_checked(name, monkeypatch):
+    """A descriptor or layout that its owner changes, or uses again for another
+    call, does not change the calls that were prepared from it."""
+    monkeypatch.setattr(L, "_here", lambda *t: None)
+    monkeypatch.setattr(L, "_prepared", lambda name, args, keep, stream: args)
+    desc, lay = _desc(), _lay()
+    args = _prepare(name, desc=desc, lay=lay)
+    lay.total_new, lay.pool_tokens, desc.n_heads_kv = 1 << 20, 1 << 30, 1 << 10
+    assert args[0]._obj.n_heads_kv == 2 and args[1]._obj.total_new == 8 and args[1]._obj.pool_tokens == 512
+
+
 # ------------------------------------------------------- the ends of integers
 
 @pytest.mark.parametrize("call", [_write, _read, _attn, _keep])
